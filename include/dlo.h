@@ -550,6 +550,95 @@ dlo_status dlo_op_adaln(const void* c, int B, int C, const void* W, const void* 
  * kernel (mode DLO_STAGE_GATHER) or cudaMemcpyAsync (DLO_STAGE_MEMCPY). */
 dlo_status dlo_op_stage(void* dst, const void* src, size_t bytes, int mode, void* stream);
 
+/* ---------------------------------------------------------------- training ops
+ * What carries gradients through the parts of a block that are not plain
+ * products: attention that keeps its row statistics and its backward pass,
+ * LayerNorm and RMSNorm with theirs.  Called like the unit ops: device
+ * pointers, enqueued on `stream` (a stream of the current device), arguments
+ * checked before any launch, no allocation, no host wait; every call may be
+ * captured into a CUDA graph.  A workspace holds nothing between calls, and
+ * calls that may run at the same time need one each.  Buffers must not
+ * overlap unless a call says so.  Results do not depend on the schedule: sums
+ * are added in a fixed order, in fp32.  Sizes are at most 2^30 rows. */
+
+/* One attention problem.  Row r of sequence b of Q starts at Q + (b * nq + r)
+ * * ldq elements, head h at column h * head_dim; K and V likewise with nk rows
+ * and head g < kv_heads; query head h reads head h / (heads / kv_heads).  So
+ * q | k | v may be one fused buffer, and so may their gradients.
+ * Query i of sequence b sees key j when i < q_lens[b], j < k_lens[b] (device
+ * int32 [batch]; NULL: nq, nk; values are taken into 0 .. nq, 0 .. nk) and, with
+ * causal_block c > 0, when floor((i + nk - nq) / c) >= floor(j / c): the last
+ * query meets the last key, c = 1 is the token-causal mask, c = tokens of a
+ * frame the frame-causal one.  What lies behind q_lens and k_lens is never
+ * used, whatever it holds.
+ * batch, heads, kv_heads, nq, nk >= 1; batch <= 65535; heads <= 65535;
+ * heads % kv_heads == 0; head_dim % 8 == 0 and <= 128; ld* % 8 == 0 and at
+ * least the row they stride; bf16 pointers 16-byte aligned. */
+typedef struct dlo_attn {
+    int batch, heads, kv_heads, head_dim, nq, nk;
+    int causal_block;                 /* 0: every key                          */
+    int ldq, ldk, ldv, ldo;           /* row strides, elements                 */
+    int lddq, lddk, lddv, lddo;       /* of the gradients (backward only)      */
+    const int* q_lens;
+    const int* k_lens;
+} dlo_attn;
+
+/* Workspace bytes of the calls below for this problem (0: bad description).
+ * They depend on the sizes alone. */
+size_t dlo_attention_fwd_workspace_bytes(const dlo_attn* a);
+size_t dlo_attention_bwd_workspace_bytes(const dlo_attn* a);
+
+/* O (bf16) = softmax(Q K^T / sqrt(head_dim)) V over the visible keys, and
+ * lse fp32 [batch, heads, nq]: the natural logarithm of the sum of
+ * exp(scores).  A query that sees no key, and every row from q_lens[b] on,
+ * gets O = 0 and lse = -inf.  err as for the unit ops. */
+dlo_status dlo_op_attention_fwd(const dlo_attn* a, const void* Q, const void* K, const void* V, void* O,
+                                float* lse, void* ws, size_t ws_bytes, int* err, void* stream);
+
+/* Gradients of dlo_op_attention_fwd: dQ, dK, dV (bf16) from its inputs, its O
+ * and lse, and dO (bf16, laid out as O with stride lddo).  The probabilities
+ * are formed again, p = exp(s - lse); ds = p (dO V^T - rowsum(dO O)).
+ * Every row is written; those behind q_lens and k_lens with zeros.  The
+ * gradients of a shared key/value head are the sums over its query heads. */
+dlo_status dlo_op_attention_bwd(const dlo_attn* a, const void* Q, const void* K, const void* V, const void* O,
+                                const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws,
+                                size_t ws_bytes, int* err, void* stream);
+
+/* dlo_op_layernorm that keeps its row statistics: mean, rstd fp32 [rows].
+ * One of the two forms or neither (shift/scale and w/b together: DLO_EINVAL).
+ * D % 4 == 0, D <= 20480; x and scale/shift 16-byte, out, w and b 8-byte
+ * aligned. */
+dlo_status dlo_op_layernorm_fwd(const float* x, int rows, int D, int rows_per_batch, const float* shift,
+                                const float* scale, int mod_ld, const void* w, const void* b, float eps,
+                                void* out, float* mean, float* rstd, void* stream);
+
+/* Gradients of dlo_op_layernorm_fwd from dy bf16 [rows, D] and its x, mean,
+ * rstd.  scale with mod_ld (modulation) or w (affine) or neither, as in the
+ * forward.  dx fp32 [rows, D] = the gradient of x plus dres fp32 [rows, D]
+ * (the gradient that reaches x past the norm; NULL: none; may be dx).
+ * dshift and dscale (both or neither; neither without a form) are written:
+ * with modulation rows of stride dmod_ld, one per batch (dmod_ld >= D,
+ * % 4); with w the gradients of b and of w, fp32 [D].  16-byte alignment for
+ * all fp32 matrices and vectors of D, 8-byte for dy and w. */
+size_t dlo_layernorm_bwd_workspace_bytes(int rows, int D, int rows_per_batch);
+dlo_status dlo_op_layernorm_bwd(const void* dy, const float* x, const float* mean, const float* rstd, int rows,
+                                int D, int rows_per_batch, const float* scale, int mod_ld, const void* w,
+                                const float* dres, float* dx, float* dshift, float* dscale, int dmod_ld,
+                                void* ws, size_t ws_bytes, void* stream);
+
+/* y = x r w, r = 1 / sqrt(mean(x^2) + eps), out of place: x bf16 rows of stride
+ * ldx, y bf16 rows of stride ldy, rstd fp32 [rows] receives r.  D % 8 == 0,
+ * D <= 20480, ld % 8 == 0, ld >= D; x, y, w 16-byte aligned. */
+dlo_status dlo_op_rmsnorm_fwd(const void* x, int ldx, int rows, int D, const void* w, float eps, void* y,
+                              int ldy, float* rstd, void* stream);
+
+/* Gradients of dlo_op_rmsnorm_fwd: dx bf16 rows of stride lddx (may be dy or x
+ * themselves, with the same stride), dw fp32 [D] or NULL. */
+size_t dlo_rmsnorm_bwd_workspace_bytes(int rows, int D);
+dlo_status dlo_op_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx, const void* w,
+                              const float* rstd, int rows, int D, void* dx, int lddx, float* dw, void* ws,
+                              size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

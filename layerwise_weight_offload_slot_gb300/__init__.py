@@ -82,6 +82,13 @@ class dlo_stats(ctypes.Structure):
         return d
 
 
+class dlo_attn(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in
+                ("batch", "heads", "kv_heads", "head_dim", "nq", "nk", "causal_block", "ldq", "ldk", "ldv",
+                 "ldo", "lddq", "lddk", "lddv", "lddo")] + [("q_lens", ctypes.c_void_p),
+                                                            ("k_lens", ctypes.c_void_p)]
+
+
 KCLASS_NAMES = ("gemm_bf16", "gemm_e4m3", "attention", "layernorm", "rmsnorm", "modulation",
                 "convert", "gather", "gemm_fp8", "quant")
 
@@ -137,6 +144,21 @@ _c = {
                               _f32, _vp, _vp),
     "dlo_op_rmsnorm": _decl("dlo_op_rmsnorm", _int, _vp, _int, _int, _int, _int, _vp, _f32, _vp),
     "dlo_op_adaln": _decl("dlo_op_adaln", _int, _vp, _int, _int, _vp, _vp, _int, _vp, _vp),
+    "dlo_attention_fwd_workspace_bytes": _decl("dlo_attention_fwd_workspace_bytes", _sz, _P(dlo_attn)),
+    "dlo_attention_bwd_workspace_bytes": _decl("dlo_attention_bwd_workspace_bytes", _sz, _P(dlo_attn)),
+    "dlo_op_attention_fwd": _decl("dlo_op_attention_fwd", _int, _P(dlo_attn), _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                                  _vp, _vp),
+    "dlo_op_attention_bwd": _decl("dlo_op_attention_bwd", _int, _P(dlo_attn), _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                  _vp, _vp, _vp, _sz, _vp, _vp),
+    "dlo_op_layernorm_fwd": _decl("dlo_op_layernorm_fwd", _int, _vp, _int, _int, _int, _vp, _vp, _int, _vp, _vp,
+                                  _f32, _vp, _vp, _vp, _vp),
+    "dlo_layernorm_bwd_workspace_bytes": _decl("dlo_layernorm_bwd_workspace_bytes", _sz, _int, _int, _int),
+    "dlo_op_layernorm_bwd": _decl("dlo_op_layernorm_bwd", _int, _vp, _vp, _vp, _vp, _int, _int, _int, _vp, _int,
+                                  _vp, _vp, _vp, _vp, _vp, _int, _vp, _sz, _vp),
+    "dlo_op_rmsnorm_fwd": _decl("dlo_op_rmsnorm_fwd", _int, _vp, _int, _int, _int, _vp, _f32, _vp, _int, _vp, _vp),
+    "dlo_rmsnorm_bwd_workspace_bytes": _decl("dlo_rmsnorm_bwd_workspace_bytes", _sz, _int, _int),
+    "dlo_op_rmsnorm_bwd": _decl("dlo_op_rmsnorm_bwd", _int, _vp, _int, _vp, _int, _vp, _vp, _int, _int, _vp, _int,
+                                _vp, _vp, _sz, _vp),
     "dlo_op_stage": _decl("dlo_op_stage", _int, _vp, _vp, _sz, _int, _vp),
 }
 
@@ -368,3 +390,63 @@ def dlo_op_adaln(c, B, C, W, bias, N, m, stream) -> None:
 
 def dlo_op_stage(dst, src, nbytes, mode, stream) -> None:
     _check(_c["dlo_op_stage"](dst, src, nbytes, mode, stream))
+
+
+# ------------------------------------------------------------------ training ops
+
+def make_attn(*, batch, heads, head_dim, nq, nk, kv_heads=None, causal_block=0, ldq, ldk, ldv, ldo,
+              lddq=0, lddk=0, lddv=0, lddo=0, q_lens=None, k_lens=None) -> dlo_attn:
+    """q_lens, k_lens: device addresses of int32 [batch] (kept alive by the caller), or None."""
+    return dlo_attn(batch, heads, heads if kv_heads is None else kv_heads, head_dim, nq, nk, causal_block,
+                    ldq, ldk, ldv, ldo, lddq, lddk, lddv, lddo, q_lens, k_lens)
+
+
+def _size(n: int) -> int:
+    if n == 0:
+        raise DloError(EINVAL, _err(None))
+    return int(n)
+
+
+def dlo_attention_fwd_workspace_bytes(a: dlo_attn) -> int:
+    return _size(_c["dlo_attention_fwd_workspace_bytes"](ctypes.byref(a)))
+
+
+def dlo_attention_bwd_workspace_bytes(a: dlo_attn) -> int:
+    return _size(_c["dlo_attention_bwd_workspace_bytes"](ctypes.byref(a)))
+
+
+def dlo_op_attention_fwd(a: dlo_attn, Q, K, V, O, lse, ws, ws_bytes, err, stream) -> None:
+    _check(_c["dlo_op_attention_fwd"](ctypes.byref(a), Q, K, V, O, lse, ws, ws_bytes, err, stream))
+
+
+def dlo_op_attention_bwd(a: dlo_attn, Q, K, V, O, lse, dO, dQ, dK, dV, ws, ws_bytes, err, stream) -> None:
+    _check(_c["dlo_op_attention_bwd"](ctypes.byref(a), Q, K, V, O, lse, dO, dQ, dK, dV, ws, ws_bytes, err,
+                                      stream))
+
+
+def dlo_op_layernorm_fwd(x, rows, D, rows_per_batch, shift, scale, mod_ld, w, b, eps, out, mean, rstd,
+                         stream) -> None:
+    _check(_c["dlo_op_layernorm_fwd"](x, rows, D, rows_per_batch, shift, scale, mod_ld, w, b, eps, out, mean,
+                                      rstd, stream))
+
+
+def dlo_layernorm_bwd_workspace_bytes(rows, D, rows_per_batch) -> int:
+    return _size(_c["dlo_layernorm_bwd_workspace_bytes"](rows, D, rows_per_batch))
+
+
+def dlo_op_layernorm_bwd(dy, x, mean, rstd, rows, D, rows_per_batch, scale, mod_ld, w, dres, dx, dshift, dscale,
+                         dmod_ld, ws, ws_bytes, stream) -> None:
+    _check(_c["dlo_op_layernorm_bwd"](dy, x, mean, rstd, rows, D, rows_per_batch, scale, mod_ld, w, dres, dx,
+                                      dshift, dscale, dmod_ld, ws, ws_bytes, stream))
+
+
+def dlo_op_rmsnorm_fwd(x, ldx, rows, D, w, eps, y, ldy, rstd, stream) -> None:
+    _check(_c["dlo_op_rmsnorm_fwd"](x, ldx, rows, D, w, eps, y, ldy, rstd, stream))
+
+
+def dlo_rmsnorm_bwd_workspace_bytes(rows, D) -> int:
+    return _size(_c["dlo_rmsnorm_bwd_workspace_bytes"](rows, D))
+
+
+def dlo_op_rmsnorm_bwd(dy, lddy, x, ldx, w, rstd, rows, D, dx, lddx, dw, ws, ws_bytes, stream) -> None:
+    _check(_c["dlo_op_rmsnorm_bwd"](dy, lddy, x, ldx, w, rstd, rows, D, dx, lddx, dw, ws, ws_bytes, stream))

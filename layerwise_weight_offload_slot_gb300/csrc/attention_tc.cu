@@ -41,8 +41,7 @@
 
 #include <cstdlib>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "attention.cuh"
 
 namespace dlo {
 
@@ -54,10 +53,9 @@ constexpr int kThreadsA = 192;
 
 template <int NB, bool TAIL, bool DUO = false>
 struct AttnPlan {
-    static constexpr int HDP = NB * 64 + (TAIL ? 16 : 0);   // padded head dim
-    static constexpr int BLK = 128 * 128;                   // 128 rows x 128 B (64 cols)
-    static constexpr int TBLK = TAIL ? 128 * 32 : 0;        // 128 rows x 32 B (16 cols)
-    static constexpr int TILE = NB * BLK + TBLK;            // one Q, K or V tile
+    static constexpr int HDP = AttnTile<NB, TAIL>::HDP;     // padded head dim
+    static constexpr int BLK = AttnTile<NB, TAIL>::BLK;     // 64 columns of a tile
+    static constexpr int TILE = AttnTile<NB, TAIL>::BYTES;  // one Q, K or V tile
     // K/V ring depth: three stages when they fit next to Q in shared memory
     // (DUO: two, so two CTAs fit on one SM)
     static constexpr int STAGES = DUO ? 2 : (TILE * 7 + 2048 <= 227 * 1024) ? 3 : 2;
@@ -80,25 +78,24 @@ struct AttnPlan {
     static_assert(!DUO || (NB == 1 && 2 * (USED + 1024) <= 228 * 1024), "DUO: two CTAs per SM");
 };
 
+// The training form (TR): masks, shared key/value heads, row statistics, and a
+// grid that may split the keys (partial results, joined by a second launch).
+struct AttnTrain {
+    float* lse;                 // [batch, heads, nq]
+    const int *q_lens, *k_lens;
+    int causal_block, group, splits;
+    float *po, *pl;             // splits > 1: [splits][batch][heads][nq][hd] and [..][nq]
+};
+
 struct AttnMaps {
     CUtensorMap q, k, v;        // 64-column boxes, 128-byte swizzle
     CUtensorMap qt, kt, vt;     // 16-column tail boxes, 32-byte swizzle
 };
 
-template <int NB, bool TAIL>
-__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* main,
-                                          const CUtensorMap* tail, int h, int row0, int b,
-                                          uint32_t bar) {
-    using P = AttnPlan<NB, TAIL>;   // BLK and TBLK do not depend on DUO
-#pragma unroll
-    for (int blk = 0; blk < NB; ++blk) tma_load_4d(dst + blk * P::BLK, main, blk * 64, h, row0, b, bar);
-    if constexpr (TAIL) tma_load_4d(dst + NB * P::BLK, tail, NB * 64, h, row0, b, bar);
-}
-
-template <int NB, bool TAIL, bool DUO>
+template <int NB, bool TAIL, bool DUO, bool TR>
 __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     attn_tc_kernel(const __grid_constant__ AttnMaps maps, __nv_bfloat16* __restrict__ O, int hd,
-                   int nq, int nk, int ldo, float scale_log2, int* err) {
+                   int nq, int nk, int ldo, float scale_log2, int* err, const AttnTrain tr) {
     using P = AttnPlan<NB, TAIL, DUO>;
     constexpr int HDP = P::HDP;
     extern __shared__ uint8_t smem_raw[];
@@ -108,7 +105,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     const uint32_t bar = sb + P::BAR_OFF;
     const uint32_t q_full = bar;
     const uint32_t kv_full = bar + 8, k_empty = bar + 32;
-    const uint32_t v_empty = bar + 80;
+    const uint32_t raw = bar + 56, v_empty = bar + 80;
     const uint32_t s_full = bar + 104;
     const uint32_t p_full = bar + 120, pv_done = bar + 128, drain = bar + 136;
     constexpr int NS = P::STAGES;
@@ -116,8 +113,41 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::ABORT_OFF);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int qt = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    const int ntiles = (nk + TK - 1) / TK;
+    const int h = blockIdx.y, b = blockIdx.z;
+    int qt = blockIdx.x, ntiles = (nk + TK - 1) / TK;
+    int t0 = 0, hk = h, qlen = nq, klen = nk, split = 0;   // TR: first key tile, key/value head, valid rows
+    if constexpr (TR) {
+        pdl_wait();             // the lengths may come from the predecessor
+        const int off = nk - nq;
+        split = qt % tr.splits;
+        // with a causal mask the last query tiles have the most keys: first
+        qt = gridDim.x / tr.splits - 1 - qt / tr.splits;
+        hk = h / tr.group;
+        qlen = seq_len(tr.q_lens, b, nq);
+        klen = seq_len(tr.k_lens, b, nk);
+        const int last = min(qt * TQ + TQ, qlen) - 1;
+        ntiles = last < qt * TQ ? 0 : (key_end(last, off, tr.causal_block, klen) + TK - 1) / TK;
+        if (tr.splits > 1) {
+            const int per = (ntiles + tr.splits - 1) / tr.splits;
+            t0 = split * per;
+            ntiles = min(ntiles, t0 + per) - t0;
+        }
+        if (ntiles <= 0) {      // no key for any of the rows
+            pdl_launch_dependents();
+            const size_t rows0 = (static_cast<size_t>(b) * gridDim.y + h) * nq;
+            if (tr.splits > 1) {
+                float* pl = tr.pl + static_cast<size_t>(split) * gridDim.z * gridDim.y * nq + rows0;
+                for (int i = qt * TQ + threadIdx.x; i < min(nq, qt * TQ + TQ); i += kThreadsA) pl[i] = -INFINITY;
+            } else {
+                const int c8 = hd / 8;
+                for (int i = threadIdx.x; i < min(nq - qt * TQ, TQ) * c8; i += kThreadsA)
+                    reinterpret_cast<uint4*>(O + (static_cast<size_t>(b) * nq + qt * TQ + i / c8) * ldo + h * hd)[i % c8] =
+                        make_uint4(0, 0, 0, 0);
+                for (int i = qt * TQ + threadIdx.x; i < min(nq, qt * TQ + TQ); i += kThreadsA) tr.lse[rows0 + i] = -INFINITY;
+            }
+            return;
+        }
+    }
 
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
@@ -130,6 +160,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         mbar_init(p_full, 4);
         mbar_init(pv_done, 1);
         mbar_init(drain, 1);
+        if constexpr (TR) mbar_init(raw, 1);
         *abort_flag = 0;
         fence_mbar_init();
         tma_prefetch_desc(&maps.q);
@@ -152,30 +183,52 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         if (err) atomicExch(err, 1);
     };
 
-    if (warp == 0 && lane == 0) {
+    // TR: keys behind k_lens end inside the last tile; their V rows become zero
+    // before the MMAs see that tile (its loads complete on `raw` instead)
+    const int fix = TR && klen < nk && klen < (t0 + ntiles) * TK ? klen - (t0 + ntiles - 1) * TK : TK;
+    if (warp == 0) {
         // ---------------- TMA producer
         bool ok = true;
         uint32_t issued = 0;      // stages with a load in flight
         uint32_t par = 0;         // parity of that load's phase
-        mbar_arrive_expect_tx(q_full, P::TILE);
-        load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * TQ, b, q_full);
-        for (int j = 0; ok && j < ntiles; ++j) {
-            const int st = j % NS;
-            const uint32_t ph = (j / NS) & 1;
-            // the stage's K is free after S_{j-NS}, its V after PV_{j-NS}
-            if (!mbar_wait(k_empty + 8 * st, ph ^ 1, abort_flag) ||
-                !mbar_wait(v_empty + 8 * st, ph ^ 1, abort_flag)) {
-                fail();
-                ok = false;
-                break;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(q_full, P::TILE);
+            load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * TQ, b, q_full);
+            for (int j = 0; ok && j < ntiles; ++j) {
+                const int st = j % NS;
+                const uint32_t ph = (j / NS) & 1;
+                // the stage's K is free after S_{j-NS}, its V after PV_{j-NS}
+                if (!mbar_wait(k_empty + 8 * st, ph ^ 1, abort_flag) ||
+                    !mbar_wait(v_empty + 8 * st, ph ^ 1, abort_flag)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                const bool raw_tile = TR && fix < TK && j == ntiles - 1;
+                const uint32_t full = raw_tile ? raw : kv_full + 8 * st;
+                mbar_arrive_expect_tx(full, 2 * P::TILE);
+                load_tile<NB, TAIL>(sb + P::K_OFF + st * P::TILE, &maps.k, &maps.kt, hk, (t0 + j) * TK, b, full);
+                load_tile<NB, TAIL>(sb + P::V_OFF + st * P::TILE, &maps.v, &maps.vt, hk, (t0 + j) * TK, b, full);
+                if (raw_tile) break;
+                issued |= 1u << st;
+                par = (par & ~(1u << st)) | (ph << st);
             }
-            mbar_arrive_expect_tx(kv_full + 8 * st, 2 * P::TILE);
-            load_tile<NB, TAIL>(sb + P::K_OFF + st * P::TILE, &maps.k, &maps.kt, h, j * TK, b, kv_full + 8 * st);
-            load_tile<NB, TAIL>(sb + P::V_OFF + st * P::TILE, &maps.v, &maps.vt, h, j * TK, b, kv_full + 8 * st);
-            issued |= 1u << st;
-            par = (par & ~(1u << st)) | (ph << st);
         }
-        if (!ok || *abort_flag) {
+        if constexpr (TR) {
+            ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+            if (ok && fix < TK) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(raw, 0, nullptr));
+                if (ok) {
+                    const int st = (ntiles - 1) % NS;
+                    zero_rows<NB, TAIL>(smem + P::V_OFF + st * P::TILE, fix, lane, 32);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(kv_full + 8 * st);
+                } else if (lane == 0) {
+                    fail();
+                }
+            }
+        }
+        if (lane == 0 && (!ok || *abort_flag)) {
             mbar_wait(q_full, 0, nullptr);
             for (int i = 0; i < NS; ++i)
                 if (issued & (1u << i)) mbar_wait(kv_full + 8 * i, (par >> i) & 1u, nullptr);
@@ -256,6 +309,11 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
         float m_ref = -INFINITY, l = 0.f;
         bool ok = true;
+        int row_end = nk;         // one past the last key of this row
+        if constexpr (TR) {
+            const int i = qt * TQ + row;
+            row_end = i < qlen ? key_end(i, nk - nq, tr.causal_block, klen) : 0;
+        }
         for (int j = 0; j < ntiles; ++j) {
             const int st = j % P::SBUF;
             const uint32_t ph = (j / P::SBUF) & 1;
@@ -277,7 +335,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
                 for (int i = 0; i < 32; ++i) v[c * 32 + i] = __uint_as_float(r[c][i]);
             // raw scores: the row max is taken before scaling (scale > 0), and
             // keys past nk exist only in the last tile
-            const int kvalid = nk - j * TK;
+            const int kvalid = row_end - (t0 + j) * TK;
             if (kvalid < TK) {
 #pragma unroll
                 for (int i = 0; i < TK; ++i)
@@ -295,7 +353,8 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             const bool resc = mt > m_ref + 8.f;
             const float m_new = resc ? mt : m_ref;
             const float corr = resc ? ex2_approx(m_ref - m_new) : 1.f;
-            const float neg = -m_new;
+            // TR: a row that has seen no key yet keeps m = -inf and p = 0
+            const float neg = TR && m_new == -INFINITY ? 0.f : -m_new;
             float sp[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < TK; ++i) {
@@ -347,8 +406,21 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             if (lane == 0) fail();
         } else {
             tc_fence_after();
-            const float inv = 1.f / l;
+            const float inv = TR && l == 0.f ? 0.f : 1.f / l;
             const int grow = qt * TQ + row;
+            float* prow = nullptr;
+            if constexpr (TR) {
+                // natural logarithm of the sum of exp(scores)
+                const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
+                const size_t r = (static_cast<size_t>(b) * gridDim.y + h) * nq + grow;
+                if (tr.splits > 1) {
+                    const size_t p = static_cast<size_t>(split) * gridDim.z * gridDim.y * nq + r;
+                    prow = tr.po + p * hd;
+                    if (grow < nq) tr.pl[p] = lse;
+                } else if (grow < nq) {
+                    tr.lse[r] = lse;
+                }
+            }
             __nv_bfloat16* orow = O + (static_cast<size_t>(b) * nq + grow) * ldo + h * hd;
 #pragma unroll 1
             for (int c = 0; c < (HDP + 31) / 32; ++c) {
@@ -358,7 +430,13 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
                 if (grow < nq) {
 #pragma unroll
                     for (int k4 = 0; k4 < 4; ++k4) {
-                        if (c * 32 + 8 * k4 < hd) {
+                        if (TR && prow && c * 32 + 8 * k4 < hd) {
+                            float4* pw = reinterpret_cast<float4*>(prow + c * 32 + 8 * k4);
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                pw[u] = make_float4(__uint_as_float(r[8 * k4 + 4 * u]) * inv, __uint_as_float(r[8 * k4 + 4 * u + 1]) * inv,
+                                                    __uint_as_float(r[8 * k4 + 4 * u + 2]) * inv, __uint_as_float(r[8 * k4 + 4 * u + 3]) * inv);
+                        } else if (c * 32 + 8 * k4 < hd) {
                             uint4 w;
                             w.x = pack_bf16x2(__uint_as_float(r[8 * k4 + 0]) * inv, __uint_as_float(r[8 * k4 + 1]) * inv);
                             w.y = pack_bf16x2(__uint_as_float(r[8 * k4 + 2]) * inv, __uint_as_float(r[8 * k4 + 3]) * inv);
@@ -381,47 +459,25 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     }
 }
 
-// [batch, rows, heads, hd] view of a bf16 matrix whose batch b, row r, head h
-// starts at base + (b * rows + r) * ld + h * hd; box of box_cols x 1 head x
-// 128 rows, columns past hd zero-filled.
-bool make_map4(CUtensorMap* m, const void* base, int batch, int rows, int heads, int hd, int ld,
-               int box_cols, CUtensorMapSwizzle sw) {
-    EncodeTiledFn enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(heads),
-                          static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
-    cuuint64_t strides[3] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(ld) * 2,
-                             static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(rows)};
-    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), 1, 128, 1};
-    cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
-               es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int NB, bool TAIL, bool DUO>
+template <int NB, bool TAIL, bool DUO, bool TR = false>
 cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int batch, int heads,
                    int hd, int nq, int nk, int ldq, int ldk, int ldv, int ldo, int* err,
-                   cudaStream_t s, unsigned long long* launches) {
+                   cudaStream_t s, unsigned long long* launches, const AttnTrain& tr = AttnTrain{nullptr, nullptr, nullptr, 0, 1, 1, nullptr, nullptr}) {
     using P = AttnPlan<NB, TAIL, DUO>;
     static_assert(P::BYTES <= 227 * 1024, "attention shared memory plan exceeds 227 KB");
-    static bool attr = false;
-    if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(attn_tc_kernel<NB, TAIL, DUO>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, P::BYTES);
-        if (e != cudaSuccess) return e;
-        attr = true;
-    }
+    const void* kernel = reinterpret_cast<const void*>(&attn_tc_kernel<NB, TAIL, DUO, TR>);
+    static unsigned long long attr = 0;
+    if (cudaError_t e = allow_smem(kernel, P::BYTES, &attr); e != cudaSuccess) return e;
     AttnMaps maps;
     const CUtensorMapSwizzle w128 = CU_TENSOR_MAP_SWIZZLE_128B, w32 = CU_TENSOR_MAP_SWIZZLE_32B;
     if (!make_map4(&maps.q, Q, batch, nq, heads, hd, ldq, 64, w128) ||
-        !make_map4(&maps.k, K, batch, nk, heads, hd, ldk, 64, w128) ||
-        !make_map4(&maps.v, V, batch, nk, heads, hd, ldv, 64, w128))
+        !make_map4(&maps.k, K, batch, nk, heads / tr.group, hd, ldk, 64, w128) ||
+        !make_map4(&maps.v, V, batch, nk, heads / tr.group, hd, ldv, 64, w128))
         return cudaErrorInvalidValue;
     if (TAIL) {
         if (!make_map4(&maps.qt, Q, batch, nq, heads, hd, ldq, 16, w32) ||
-            !make_map4(&maps.kt, K, batch, nk, heads, hd, ldk, 16, w32) ||
-            !make_map4(&maps.vt, V, batch, nk, heads, hd, ldv, 16, w32))
+            !make_map4(&maps.kt, K, batch, nk, heads / tr.group, hd, ldk, 16, w32) ||
+            !make_map4(&maps.vt, V, batch, nk, heads / tr.group, hd, ldv, 16, w32))
             return cudaErrorInvalidValue;
     } else {
         maps.qt = maps.q;
@@ -429,8 +485,8 @@ cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int bat
         maps.vt = maps.v;
     }
     const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
-    dim3 grid((nq + TQ - 1) / TQ, heads, batch);
-    cudaError_t le_ = launch_k(attn_tc_kernel<NB, TAIL, DUO>, grid, kThreadsA, P::BYTES, s, maps, static_cast<__nv_bfloat16*>(O), hd, nq, nk, ldo, scale_log2, err);
+    dim3 grid((nq + TQ - 1) / TQ * tr.splits, heads, batch);
+    cudaError_t le_ = launch_k(attn_tc_kernel<NB, TAIL, DUO, TR>, grid, kThreadsA, P::BYTES, s, maps, static_cast<__nv_bfloat16*>(O), hd, nq, nk, ldo, scale_log2, err, tr);
     ++*launches;
     return le_ != cudaSuccess ? le_ : cudaGetLastError();
 }
@@ -465,6 +521,86 @@ cudaError_t launch_attention_tc(const void* Q, const void* K, const void* V, voi
         return duo ? run_tc<1, true, true>(Q, K, V, O, batch, heads, hd, nq, nk, ldq, ldk, ldv, ldo, err, s, launches)
                    : run_tc<1, true, false>(Q, K, V, O, batch, heads, hd, nq, nk, ldq, ldk, ldv, ldo, err, s, launches);
     return run_tc<2, false, false>(Q, K, V, O, batch, heads, hd, nq, nk, ldq, ldk, ldv, ldo, err, s, launches);
+}
+
+namespace {
+
+// Joins the partial results of a split: lse = log sum_p exp(lse_p), O = sum_p
+// exp(lse_p - lse) O_p.  One warp a row; bound by reading the partial rows.
+__global__ void __launch_bounds__(256) attn_join_kernel(const float* __restrict__ po, const float* __restrict__ pl,
+                                                        int splits, size_t rows, int nq, int heads, int hd,
+                                                        __nv_bfloat16* __restrict__ O, int ldo,
+                                                        float* __restrict__ lse) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int lane = threadIdx.x & 31;
+    const size_t r = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;     // (b, h, i)
+    if (r >= rows) return;
+    float top = -INFINITY;
+    for (int p = 0; p < splits; ++p) top = fmaxf(top, pl[p * rows + r]);
+    const float m = top == -INFINITY ? 0.f : top;
+    float total = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);      // columns 4 lane .. 4 lane + 3
+    for (int p = 0; p < splits; ++p) {
+        const float w = exp2f((pl[p * rows + r] - m) * 1.4426950408889634f);
+        if (w == 0.f) continue;                        // nothing visible there: its O_p was not written
+        total += w;
+        if (4 * lane < hd) {
+            const float4 v = reinterpret_cast<const float4*>(po + (p * rows + r) * hd)[lane];
+            acc = make_float4(acc.x + w * v.x, acc.y + w * v.y, acc.z + w * v.z, acc.w + w * v.w);
+        }
+    }
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+    const size_t bh = r / nq, i = r - bh * nq, b = bh / heads, h = bh - b * heads;
+    if (4 * lane < hd)
+        reinterpret_cast<uint2*>(O + (b * nq + i) * ldo + h * hd)[lane] =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0) lse[r] = total == 0.f ? -INFINITY : m + logf(total);
+}
+
+// CTAs that share the keys of one query tile: as many as fill the SMs when the
+// query tiles alone do not, each with at least four key tiles.  Sizes only.
+int attn_fwd_splits(const dlo_attn& a) {
+    const long long ctas = static_cast<long long>((a.nq + TQ - 1) / TQ) * a.heads * a.batch;
+    const long long fill = kGb300Sms / ctas, tiles = (a.nk + TK - 1) / TK / 4;
+    const long long n = fill < tiles ? fill : tiles;
+    return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+}
+
+}  // namespace
+
+size_t attention_fwd_workspace(const dlo_attn& a) {
+    const size_t rows = static_cast<size_t>(a.batch) * a.heads * a.nq;
+    const int n = attn_fwd_splits(a);
+    return 256 + (n > 1 ? n * rows * (a.head_dim + 1) * sizeof(float) : 0);
+}
+
+cudaError_t launch_attention_fwd(const dlo_attn& a, const void* Q, const void* K, const void* V, void* O, float* lse,
+                                 void* ws, int* err, cudaStream_t s, unsigned long long* launches) {
+    const size_t rows = static_cast<size_t>(a.batch) * a.heads * a.nq;
+    AttnTrain tr = {lse, a.q_lens, a.k_lens, a.causal_block < a.nk ? a.causal_block : a.nk, a.heads / a.kv_heads,
+                    attn_fwd_splits(a), static_cast<float*>(ws), nullptr};
+    tr.pl = tr.po + tr.splits * rows * a.head_dim;
+    const int hd = a.head_dim;
+    const long long ctas = static_cast<long long>((a.nq + TQ - 1) / TQ) * a.heads * a.batch * tr.splits;
+    const bool duo = ctas > kGb300Sms;      // as for launch_attention_tc
+    cudaError_t e;
+#define DLO_AF(NB, TAIL, DUO)                                                                                         e = run_tc<NB, TAIL, DUO, true>(Q, K, V, O, a.batch, a.heads, hd, a.nq, a.nk, a.ldq, a.ldk, a.ldv, a.ldo, err,                                     s, launches, tr)
+    if (hd <= 64) {
+        if (duo) DLO_AF(1, false, true);
+        else DLO_AF(1, false, false);
+    } else if (hd <= 80) {
+        if (duo) DLO_AF(1, true, true);
+        else DLO_AF(1, true, false);
+    } else {
+        DLO_AF(2, false, false);
+    }
+#undef DLO_AF
+    if (e != cudaSuccess || tr.splits == 1) return e;
+    e = launch_k(attn_join_kernel, static_cast<unsigned>((rows + 7) / 8), 256, 0, s, tr.po, tr.pl, tr.splits, rows, a.nq,
+                 a.heads, hd, static_cast<__nv_bfloat16*>(O), a.ldo, lse);
+    ++*launches;
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_attention(const void* Q, const void* K, const void* V, void* O, int batch,

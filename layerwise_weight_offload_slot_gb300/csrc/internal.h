@@ -167,7 +167,8 @@ cudaError_t launch_attention_tc(const void* Q, const void* K, const void* V, voi
 
 cudaError_t launch_layernorm(const float* x, int rows, int D, int rpb, const float* shift,
                              const float* scale, int mod_ld, const void* w, const void* b,
-                             float eps, void* out, cudaStream_t s, unsigned long long* launches);
+                             float eps, void* out, cudaStream_t s, unsigned long long* launches,
+                             float* mean = nullptr, float* rstd = nullptr);
 cudaError_t launch_rmsnorm(void* x, int rows, int D, int ld, int col0, const void* w, float eps,
                            cudaStream_t s, unsigned long long* launches);
 // Two segments of one row set in one launch (q and k of the same rows).
@@ -199,5 +200,31 @@ cudaError_t launch_quantize_e4m3(const void* x, int rows, int cols, int ld, void
 // *out += sum of the 64-bit words of src (bytes % 16 == 0), mod 2^64.
 cudaError_t launch_checksum(const void* src, size_t bytes, unsigned long long* out, cudaStream_t s,
                             unsigned long long* launches);
+
+// SMs of a GB300: the training forms' plans (grids, splits, workspace sizes)
+// follow from the sizes alone, without a device.
+constexpr int kGb300Sms = 152;
+
+// Training forms (norm_train.cu).  Workspace sizes depend on the sizes alone.
+size_t layernorm_bwd_workspace(int rows, int D, int rpb);
+size_t rmsnorm_bwd_workspace(int rows, int D);
+cudaError_t launch_layernorm_bwd(const void* dy, const float* x, const float* mean, const float* rstd, int rows, int D,
+                                 int rpb, const float* scale, int mod_ld, const void* w, const float* dres, float* dx,
+                                 float* dshift, float* dscale, int dmod_ld, float* ws, cudaStream_t s,
+                                 unsigned long long* launches);
+cudaError_t launch_rmsnorm_fwd(const void* x, int ldx, int rows, int D, const void* w, float eps, void* y, int ldy,
+                               float* rstd, cudaStream_t s, unsigned long long* launches);
+cudaError_t launch_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx, const void* w, const float* rstd,
+                               int rows, int D, void* dx, int lddx, float* dw, float* ws, cudaStream_t s,
+                               unsigned long long* launches);
+
+// Training attention (attention_tc.cu, attention_bwd.cu).  The problem is checked by the callers.
+size_t attention_fwd_workspace(const dlo_attn& a);
+size_t attention_bwd_workspace(const dlo_attn& a);
+cudaError_t launch_attention_fwd(const dlo_attn& a, const void* Q, const void* K, const void* V, void* O, float* lse,
+                                 void* ws, int* err, cudaStream_t s, unsigned long long* launches);
+cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K, const void* V, const void* O,
+                                 const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
+                                 cudaStream_t s, unsigned long long* launches);
 
 }  // namespace dlo

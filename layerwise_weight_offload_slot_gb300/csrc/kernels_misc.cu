@@ -47,7 +47,9 @@ __global__ void __launch_bounds__(256) layernorm_kernel(const float* __restrict_
                                                         const __nv_bfloat16* __restrict__ w,
                                                         const __nv_bfloat16* __restrict__ b,
                                                         float eps,
-                                                        __nv_bfloat16* __restrict__ out) {
+                                                        __nv_bfloat16* __restrict__ out,
+                                                        float* __restrict__ mean_out,
+                                                        float* __restrict__ rstd_out) {
     pdl_wait();
     pdl_launch_dependents();
     constexpr int RPC = 8 / WPR;                  // rows per 256-thread CTA
@@ -111,6 +113,10 @@ __global__ void __launch_bounds__(256) layernorm_kernel(const float* __restrict_
     if (!live) return;
     const float var = q / static_cast<float>(D);
     const float rstd = rsqrtf(var + eps);
+    if (mean_out && t0 == 0) {
+        mean_out[row] = mean;
+        rstd_out[row] = rstd;
+    }
     uint2* orow = reinterpret_cast<uint2*>(out + static_cast<size_t>(row) * D);
 #pragma unroll
     for (int j = 0; j < V4; ++j) {
@@ -528,7 +534,8 @@ inline unsigned blocks_for(size_t threads, unsigned per) {
 
 cudaError_t launch_layernorm(const float* x, int rows, int D, int rpb, const float* shift,
                              const float* scale, int mod_ld, const void* w, const void* b,
-                             float eps, void* out, cudaStream_t s, unsigned long long* launches) {
+                             float eps, void* out, cudaStream_t s, unsigned long long* launches,
+                             float* mean, float* rstd) {
     if (rows <= 0) return cudaSuccess;
     // DLO_LN_WPR=1|2|4|8 forces the warps per row (tuning)
     static int forced = -1;
@@ -553,7 +560,7 @@ cudaError_t launch_layernorm(const float* x, int rows, int D, int rpb, const flo
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(out);
     cudaError_t le_ = cudaErrorInvalidValue;
 #define DLO_LN(V, W) \
-    le_ = launch_k(layernorm_kernel<V, W>, g, 256, 0, s, x, rows, D, rpb, shift, scale, mod_ld, wb, bb, eps, o)
+    le_ = launch_k(layernorm_kernel<V, W>, g, 256, 0, s, x, rows, D, rpb, shift, scale, mod_ld, wb, bb, eps, o, mean, rstd)
     if (wpr == 1) {
         if (v4 <= 2) DLO_LN(2, 1);
         else if (v4 <= 4) DLO_LN(4, 1);
