@@ -16,11 +16,11 @@
 //               S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q
 //
 // In both, dS (and P) is the A operand straight from tensor memory: the
-// thread that owns a TMEM lane (a query row, a key) reads 64 columns of the
+// thread that owns a TMEM lane (a query row, a key) reads 32 columns of the
 // fp32 product and writes their bf16 values over the columns it has read.  The
 // B operands of the accumulating products are the tiles already in shared
-// memory, read MN-major.  12 warps: 0 TMA, 1 MMA issue, 4..11 elementwise (two
-// per 32 TMEM lanes, each half of the 128 columns).  The products of tile j + 1
+// memory, read MN-major.  20 warps: 0 TMA, 1 MMA issue, 4..19 elementwise (four
+// per 32 TMEM lanes, each a quarter of the 128 columns).  The products of tile j + 1
 // that do not wait for the elementwise work of tile j are issued before those
 // that do, so the tensor core computes while the elementwise warps run.
 //
@@ -38,8 +38,13 @@ namespace dlo {
 namespace {
 
 constexpr int kTile = 128;
-constexpr int kThreadsB = 384;
-constexpr int kStatBytes = 2 * kTile * sizeof(float);   // L and D of one query tile
+constexpr int kGroups = 4;                               // warps that share 32 TMEM lanes
+constexpr int kCols = kTile / kGroups;                   // columns of each
+constexpr int kThreadsB = 128 + 32 * 4 * kGroups;
+// Row statistics of one query tile as the operand of one more step of 16 of a
+// product: 128 rows x 16 bf16 (32-byte rows, 32-byte swizzle), columns 0..2 the
+// three bf16 parts of -L, 3..5 those of -D.
+constexpr int kStatBytes = kTile * 32;
 
 struct BwdMaps {
     CUtensorMap q, k, v, d;       // 64-column boxes, 128-byte swizzle (d: dO)
@@ -52,44 +57,64 @@ struct BwdArgs {
     float scale, scale_log2;      // 1 / sqrt(hd), log2(e) / sqrt(hd)
     const __nv_bfloat16 *O, *dO;
     const float* lse;
-    float* stats;                 // [batch * heads][query tiles][L 128 | D 128]
+    uint4* stats;                 // [batch * heads][query tiles] operands of kStatBytes
     __nv_bfloat16 *dQ, *dK, *dV;
     int ldo, lddo, lddq, lddk, lddv;
     int* err;
 };
 
-template <int NB, bool TAIL>
+// Shared memory of one CTA: two tiles that stay (Q and dO; K and V), two
+// rings that move (K and V; Q and dO), operand tiles for bf16 dS and P, and
+// per-row statistics.  DQ: the plan of dq_kernel.
+//
+// Ring depths: a tile of ring 0 is held from its first product to the last one
+// of the iteration, one of ring 1 shorter, and a reload takes ~1 us from L2.
+// Three and two stages hide it; dkv_kernel at head dims over 80 has room for
+// two and two.
+template <int NB, bool TAIL, bool DQ>
 struct BwdPlan {
     using T = AttnTile<NB, TAIL>;
     static constexpr int TILE = T::BYTES;
-    // two tiles stay (Q and dO, or K and V), two rings move
-    static constexpr int STAGES = NB == 2 ? 2 : 3;
+    static constexpr int S0 = DQ || NB == 1 ? 3 : 2, S1 = 2;
+    // dkv_kernel's tensor memory: S^T [0, 128), dP^T [128, 256), then dV and dK, then P^T
+    // and dS^T (64 columns each) where 512 columns hold them.  A P or dS that
+    // takes the place of its product instead makes the next product wait for it.
+    static constexpr uint32_t DV_COL = 256, DK_COL = DV_COL + T::HDP;
+    static constexpr uint32_t FREE = 512 - DK_COL - T::HDP;
+    static constexpr bool P_APART = FREE >= 64, DS_APART = FREE >= 128;
+    static constexpr uint32_t P_COL = P_APART ? DK_COL + T::HDP : 0;
+    static constexpr uint32_t DS_COL = DS_APART ? P_COL + 64 : 128;
     static constexpr int A0_OFF = 0, A1_OFF = TILE;
     static constexpr int R0_OFF = 2 * TILE;
-    static constexpr int R1_OFF = R0_OFF + STAGES * TILE;
-    static constexpr int STAT_OFF = R1_OFF + STAGES * TILE;
-    static constexpr int BAR_OFF = STAT_OFF + STAGES * kStatBytes;
-    // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, then full0, full1, empty0, empty1 of each stage
-    static constexpr int NBARS = 10 + 4 * STAGES;
+    static constexpr int R1_OFF = R0_OFF + S0 * TILE;
+    // dq: partial sums of D; dkv: the two selecting operands, then statistics per ring-0 stage
+    static constexpr int SEL_OFF = R1_OFF + S1 * TILE;
+    static constexpr int STAT_OFF = SEL_OFF + 2 * kStatBytes;
+    static constexpr int BAR_OFF = DQ ? SEL_OFF + kGroups * kTile * 4 : STAT_OFF + S0 * kStatBytes;
+    // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, s_read, d_read; full0, empty0 [S0]; full1, empty1 [S1]
+    static constexpr int NBARS = 12 + 2 * S0 + 2 * S1;
     static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
     static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
-    static constexpr int USED = ABORT_OFF + 4 + 1024;
-    // one CTA per SM: it owns all 512 TMEM columns
-    static constexpr int BYTES = USED > 118784 ? USED : 118784;
-    static_assert(BYTES <= 227 * 1024, "attention backward shared memory plan exceeds 227 KB");
+    static constexpr int USED = ABORT_OFF + 4;
+    // one CTA per SM (it owns all 512 TMEM columns); 1 KB to align the base
+    // where there is room, else the kernel checks that the base is aligned
+    static constexpr int WANT = USED + 1024 > 118784 ? USED + 1024 : 118784;
+    static constexpr int BYTES = WANT < 227 * 1024 ? WANT : 227 * 1024;
+    static_assert(USED <= 227 * 1024, "attention backward shared memory plan exceeds 227 KB");
+    static_assert(DK_COL + T::HDP <= 512, "attention backward tensor memory plan");
 };
 
 struct BwdBars {
-    uint32_t a_full, raw0, raw1, s_full, d_full, e0, e1, done, drain, full0, full1, empty0, empty1;
+    uint32_t a_full, raw0, raw1, s_full, d_full, e0, e1, done, drain, s_read, d_read, full0, empty0, full1, empty1;
 };
 
-template <int STAGES>
+template <int S0, int S1>
 __device__ __forceinline__ BwdBars bwd_bars(uint32_t b) {
-    return {b, b + 8, b + 16, b + 24, b + 40, b + 48, b + 56, b + 64, b + 72,
-            b + 80, b + 80 + 8 * STAGES, b + 80 + 16 * STAGES, b + 80 + 24 * STAGES};
+    return {b, b + 8, b + 16, b + 24, b + 40, b + 48, b + 56, b + 64, b + 72, b + 80, b + 88,
+            b + 96, b + 96 + 8 * S0, b + 96 + 16 * S0, b + 96 + 16 * S0 + 8 * S1};
 }
 
-template <int STAGES>
+template <int S0, int S1>
 __device__ __forceinline__ void bwd_init(const BwdBars& m) {
     mbar_init(m.a_full, 1);
     mbar_init(m.raw0, 1);
@@ -97,17 +122,26 @@ __device__ __forceinline__ void bwd_init(const BwdBars& m) {
     mbar_init(m.s_full, 1);
     mbar_init(m.s_full + 8, 1);
     mbar_init(m.d_full, 1);
-    mbar_init(m.e0, 8);
-    mbar_init(m.e1, 8);
+    mbar_init(m.e0, 4 * kGroups);
+    mbar_init(m.e1, 4 * kGroups);
+    mbar_init(m.s_read, 4 * kGroups);
+    mbar_init(m.d_read, 4 * kGroups);
     mbar_init(m.done, 1);
     mbar_init(m.drain, 1);
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < S0; ++i) {
         mbar_init(m.full0 + 8 * i, 1);
-        mbar_init(m.full1 + 8 * i, 1);
         mbar_init(m.empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < S1; ++i) {
+        mbar_init(m.full1 + 8 * i, 1);
         mbar_init(m.empty1 + 8 * i, 1);
     }
     fence_mbar_init();
+}
+
+// mbar_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
 
 // Loads of a ring in flight, for the drain: stages and the parity of each.
@@ -137,23 +171,31 @@ __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t at, 
     if constexpr (TAIL) tc_mma_f16(d, at, bt, id, 1u);
 }
 
-// 128 x hd += A B: A in TMEM (bf16 pairs: contracted indices 0..63 at a, 64..127
-// at a + 64), B a tile of shared memory whose rows are the contracted index.
-template <int NB, bool TAIL>
+// 128 x hd += A B: A in TMEM (bf16 pairs: the kCols contracted indices of group
+// e at a + GAP e), B a tile of shared memory whose rows are the contracted index.
+template <int NB, bool TAIL, int GAP>
 __device__ __forceinline__ void mma_accumulate(uint32_t d, uint32_t a, uint64_t b, uint64_t bt, bool first) {
     constexpr uint32_t id = idesc_bf16_f32(kTile, NB * 64, true);
     constexpr uint32_t idt = idesc_bf16_f32(kTile, 16, true);
 #pragma unroll
     for (int kk = 0; kk < kTile / 16; ++kk) {
-        const uint32_t ak = a + (kk >> 2) * 64 + (kk & 3) * 8;
+        const uint32_t ak = a + kk / (kCols / 16) * GAP + kk % (kCols / 16) * 8;
         const uint32_t acc = (!first || kk > 0) ? 1u : 0u;
         tc_mma_f16_ts(d, ak, b + ((kk * 2048) >> 4), id, acc);
         if constexpr (TAIL) tc_mma_f16_ts(d + NB * 64, ak, bt + ((kk * 512) >> 4), idt, acc);
     }
 }
 
-// One thread's part of an accumulator row (32-column chunks c with c % 2 ==
-// half, or all of them) times `scale`, as bf16.
+// x as the sum of three bf16 values (to ~2^-24 of x), two of them in one word.
+__device__ __forceinline__ void split3(float x, uint32_t& hi_mid, uint32_t& lo) {
+    const float a = __bfloat162float(__float2bfloat16_rn(x));
+    const float b = __bfloat162float(__float2bfloat16_rn(x - a));
+    hi_mid = pack_bf16x2(a, b);
+    lo = __bfloat16_as_ushort(__float2bfloat16_rn(x - a - b));
+}
+
+// One thread's part of an accumulator row (32-column chunks first, first +
+// step, ...) times `scale`, as bf16.
 template <int HDP>
 __device__ __forceinline__ void store_row(uint32_t t, __nv_bfloat16* out, int hd, bool live, float scale, int first,
                                           int step) {
@@ -195,6 +237,19 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
     return t;
 }
 
+// A raw score that no score makes up for: exp of it is 0, and times 0 it is 0.
+constexpr float kNothing = -1e30f;
+
+// Row `r` of a statistics operand.
+__device__ __forceinline__ void write_stat(uint4* stat, int r, float neg_l, float neg_d) {
+    uint32_t l01, l2, d01, d2;
+    split3(neg_l, l01, l2);
+    split3(neg_d, d01, d2);
+    const int x = (r >> 2) & 1;          // 32-byte swizzle: the row's two pieces change places
+    stat[2 * r + x] = make_uint4(l01, l2 | (d01 << 16), (d01 >> 16) | (d2 << 16), 0);
+    stat[2 * r + 1 - x] = make_uint4(0, 0, 0, 0);
+}
+
 // ------------------------------------------------------------------ dQ
 // TMEM: S in two buffers [0, 128) and [128, 256), dP [256, 384), dQ [384, 512).
 // Issue order S_0 dP_0 | S_1 . dP_1 dQ_0 | S_2 . dP_2 dQ_1 | ... where "." waits
@@ -202,16 +257,20 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
 template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
-    using P = BwdPlan<NB, TAIL>;
+    using P = BwdPlan<NB, TAIL, true>;
     using T = AttnTile<NB, TAIL>;
-    constexpr int NS = P::STAGES;
+    constexpr int N0 = P::S0, N1 = P::S1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sb = smem_u32(smem);
-    const BwdBars m = bwd_bars<NS>(sb + P::BAR_OFF);
+    const BwdBars m = bwd_bars<N0, N1>(sb + P::BAR_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + P::TMEM_SLOT_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::ABORT_OFF);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem - smem_raw + P::USED > P::BYTES) {       // the base of dynamic shared memory is 1 KB aligned
+        if (threadIdx.x == 0 && g.err) atomicExch(g.err, 1);
+        return;
+    }
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     // with a causal mask the last query tiles see the most keys: first
     const int qt = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int row0 = qt * kTile, off = g.nk - g.nq;
@@ -220,19 +279,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int qlen = seq_len(g.q_lens, b, g.nq), klen = seq_len(g.k_lens, b, g.nk);
     const int last = min(row0 + kTile, qlen) - 1;
     const int n = last < row0 ? 0 : (key_end(last, off, g.causal_block, klen) + kTile - 1) / kTile;
-    float* stat = g.stats + ((static_cast<size_t>(b) * g.heads + h) * gridDim.x + qt) * 2 * kTile;
+    uint4* stat = g.stats + ((static_cast<size_t>(b) * g.heads + h) * gridDim.x + qt) * (kStatBytes / 16);
     __nv_bfloat16* dq0 = g.dQ + (static_cast<size_t>(b) * g.nq + row0) * g.lddq + h * g.hd;
     if (n <= 0) {
-        if (threadIdx.x < kTile) {
-            stat[threadIdx.x] = INFINITY;
-            stat[kTile + threadIdx.x] = 0.f;
-        }
+        if (threadIdx.x < kTile) write_stat(stat, threadIdx.x, kNothing, 0.f);
         zero_out(dq0, g.lddq, min(kTile, g.nq - row0), g.hd);
         return;
     }
 
     if (threadIdx.x == 0) {
-        bwd_init<NS>(m);
+        bwd_init<N0, N1>(m);
         *abort_flag = 0;
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
@@ -246,7 +302,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
     // only now: the next kernel's CTAs may allocate TMEM before they wait for
     // this grid, so every CTA of this one must hold its own first
     pdl_launch_dependents();
@@ -268,29 +324,29 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, row0, b, m.a_full);
             load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, row0, b, m.a_full);
             for (int j = 0; j < n; ++j) {
-                const int st = j % NS;
-                const uint32_t ph = (j / NS) & 1;
+                const int st = j % N0, sv = j % N1;
+                const uint32_t ph = (j / N0) & 1, pv = (j / N1) & 1;
                 if (!mbar_wait(m.empty0 + 8 * st, ph ^ 1, abort_flag)) { ok = false; break; }
                 const bool raw = fix < kTile && j == n - 1;
                 const uint32_t full = raw ? m.raw0 : m.full0 + 8 * st;
                 mbar_arrive_expect_tx(full, P::TILE);
                 load_tile<NB, TAIL>(sb + P::R0_OFF + st * P::TILE, &maps.k, &maps.kt, hk, j * kTile, b, full);
                 if (!raw) f0.add(st, ph);
-                if (!mbar_wait(m.empty1 + 8 * st, ph ^ 1, abort_flag)) {
+                if (!mbar_wait(m.empty1 + 8 * sv, pv ^ 1, abort_flag)) {
                     ok = false;
                     if (raw) mbar_wait(m.raw0, 0, nullptr);
                     break;
                 }
-                mbar_arrive_expect_tx(m.full1 + 8 * st, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R1_OFF + st * P::TILE, &maps.v, &maps.vt, hk, j * kTile, b, m.full1 + 8 * st);
-                f1.add(st, ph);
+                mbar_arrive_expect_tx(m.full1 + 8 * sv, P::TILE);
+                load_tile<NB, TAIL>(sb + P::R1_OFF + sv * P::TILE, &maps.v, &maps.vt, hk, j * kTile, b, m.full1 + 8 * sv);
+                f1.add(sv, pv);
             }
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (ok && fix < kTile) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(m.raw0, 0, nullptr));
             if (ok) {
-                const int st = (n - 1) % NS;
+                const int st = (n - 1) % N0;
                 zero_rows<NB, TAIL>(smem + P::R0_OFF + st * P::TILE, fix, lane, 32);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m.full0 + 8 * st);
@@ -300,115 +356,128 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (!ok) fail();
             if (*abort_flag) {
                 mbar_wait(m.a_full, 0, nullptr);
-                f0.drain<NS>(m.full0);
-                f1.drain<NS>(m.full1);
+                f0.drain<N0>(m.full0);
+                f1.drain<N1>(m.full1);
             }
         }
-    } else if (warp == 1 && lane == 0) {
-        // ---------------- MMA issuer
+    } else if (warp == 1) {
+        // ---------------- MMA issuer: the warp waits, one lane issues
+        const bool one = elect_one();
         const uint64_t q = sw128_kmajor_desc(sb + P::A0_OFF), qtl = sw32_desc(sb + P::A0_OFF + NB * T::BLK);
         const uint64_t d = sw128_kmajor_desc(sb + P::A1_OFF), dtl = sw32_desc(sb + P::A1_OFF + NB * T::BLK);
         const uint64_t k = sw128_kmajor_desc(sb + P::R0_OFF), kmn = sw128_mnmajor_desc(sb + P::R0_OFF, T::BLK);
         const uint64_t ktl = sw32_desc(sb + P::R0_OFF + NB * T::BLK);
         const uint64_t v = sw128_kmajor_desc(sb + P::R1_OFF), vtl = sw32_desc(sb + P::R1_OFF + NB * T::BLK);
         auto issue_s = [&](int j) -> bool {
-            const int st = j % NS;
-            if (!mbar_wait(m.full0 + 8 * st, (j / NS) & 1, abort_flag)) return false;
+            const int st = j % N0;
+            if (!warp_wait(m.full0 + 8 * st, (j / N0) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint32_t so = (st * P::TILE) >> 4;
-            mma_scores<NB, TAIL>(tmem + (j & 1) * 128, q, qtl, k + so, ktl + so);
-            tc_commit(m.s_full + 8 * (j & 1));
+            if (one) {
+                mma_scores<NB, TAIL>(tmem + (j & 1) * 128, q, qtl, k + so, ktl + so);
+                tc_commit(m.s_full + 8 * (j & 1));
+            }
+            __syncwarp();
             return true;
         };
         auto issue_dp = [&](int j) -> bool {
-            const int st = j % NS;
-            if (!mbar_wait(m.full1 + 8 * st, (j / NS) & 1, abort_flag)) return false;
+            const int st = j % N1;
+            if (!warp_wait(m.full1 + 8 * st, (j / N1) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint32_t so = (st * P::TILE) >> 4;
-            mma_scores<NB, TAIL>(tmem + 256, d, dtl, v + so, vtl + so);
-            tc_commit(m.d_full);
-            tc_commit(m.empty1 + 8 * st);
+            if (one) {
+                mma_scores<NB, TAIL>(tmem + 256, d, dtl, v + so, vtl + so);
+                tc_commit(m.d_full);
+                tc_commit(m.empty1 + 8 * st);
+            }
+            __syncwarp();
             return true;
         };
-        bool ok = mbar_wait(m.a_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
+        bool ok = warp_wait(m.a_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
         for (int j = 0; ok && j < n; ++j) {
-            // S_{j+1} overwrites dS_{j-1}, which dQ_{j-1}, issued before, has read
-            if (j + 1 < n && !issue_s(j + 1)) ok = false;
-            if (ok && !mbar_wait(m.e0, j & 1, abort_flag)) ok = false;
-            if (!ok) break;
+            if (j + 1 < n) {
+                // S_{j+1} overwrites dS_{j-1}, which dQ_{j-1}, issued before, reads
+                ok = issue_s(j + 1) && warp_wait(m.d_read, j & 1, abort_flag) && issue_dp(j + 1);
+                if (!ok) break;
+            }
+            if (!warp_wait(m.e0, j & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            if (j + 1 < n && !issue_dp(j + 1)) { ok = false; break; }
-            const int st = j % NS;
+            const int st = j % N0;
             const uint32_t so = (st * P::TILE) >> 4;
-            mma_accumulate<NB, TAIL>(tmem + 384, tmem + (j & 1) * 128, kmn + so, ktl + so, j == 0);
-            tc_commit(m.empty0 + 8 * st);
+            if (one) {
+                mma_accumulate<NB, TAIL, kCols>(tmem + 384, tmem + (j & 1) * 128, kmn + so, ktl + so, j == 0);
+                tc_commit(m.empty0 + 8 * st);
+            }
+            __syncwarp();
         }
-        if (ok) tc_commit(m.done);
-        else fail();
-        if (*abort_flag) {
-            tc_commit(m.drain);
-            mbar_wait(m.drain, 0, nullptr);
+        if (one) {
+            if (ok) tc_commit(m.done);
+            else fail();
+            if (*abort_flag) {
+                tc_commit(m.drain);
+                mbar_wait(m.drain, 0, nullptr);
+            }
         }
+        __syncwarp();
     } else if (warp >= 4) {
         // ---------------- elementwise: thread = query row, half of the columns
-        const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;    // group, TMEM lane
         const int i = row0 + row;
         const bool valid = i < qlen;
         const int end = valid ? key_end(i, off, g.causal_block, klen) : 0;
-        // D = rowsum(dO O): each half of the threads adds half of the columns
-        float* part = reinterpret_cast<float*>(smem + P::STAT_OFF);
+        // D = rowsum(dO O): each group adds a part of the columns
+        float* part = reinterpret_cast<float*>(smem + P::SEL_OFF);
         float delta = 0.f;
         if (valid) {
             const uint4* o = reinterpret_cast<const uint4*>(g.O + (static_cast<size_t>(b) * g.nq + i) * g.ldo + h * g.hd);
-            const uint4* e = reinterpret_cast<const uint4*>(g.dO + (static_cast<size_t>(b) * g.nq + i) * g.lddo + h * g.hd);
-            for (int c = half; c < g.hd / 8; c += 2) delta += dot8(o[c], e[c]);
+            const uint4* d = reinterpret_cast<const uint4*>(g.dO + (static_cast<size_t>(b) * g.nq + i) * g.lddo + h * g.hd);
+            for (int c = e; c < g.hd / 8; c += kGroups) delta += dot8(o[c], d[c]);
         }
-        part[half * kTile + row] = delta;
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        delta = part[row] + part[kTile + row];
+        part[e * kTile + row] = delta;
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreadsB - 128) : "memory");
+        delta = 0.f;
+#pragma unroll
+        for (int c = 0; c < kGroups; ++c) delta += part[c * kTile + row];
         float l2 = INFINITY;
         if (valid) {
             const float l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
             if (l != -INFINITY) l2 = l * 1.4426950408889634f;
         }
-        if (half == 0) {
-            stat[row] = l2;
-            stat[kTile + row] = delta;
-        }
-        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 64 * half;
+        // -L in units of the raw score
+        if (e == 0) write_stat(stat, row, l2 == INFINITY ? kNothing : -l2 / g.scale_log2, -delta);
+        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            const uint32_t ts = tl + (j & 1) * 128;
+            const uint32_t ts = tl + (j & 1) * 128 + kCols * e;
             bool got = mbar_wait(m.s_full + 8 * (j & 1), (j >> 1) & 1, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
             tc_fence_after();
-            uint32_t r[2][32];
-            tmem_ld_32x32b_x32(ts, r[0]);
-            tmem_ld_32x32b_x32(ts + 32, r[1]);
-            tmem_wait_ld_r(r[0]);
-            tmem_wait_ld_r(r[1]);
-            float p[64];
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(ts, r);
+            tmem_wait_ld_r(r);
+            float p[32];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) p[c] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][c & 31]), g.scale_log2, -l2));
+            for (int c = 0; c < 32; ++c) p[c] = ex2_approx(fmaf(__uint_as_float(r[c]), g.scale_log2, -l2));
             got = mbar_wait(m.d_full, j & 1, abort_flag);
             if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
             tc_fence_after();
-            tmem_ld_32x32b_x32(tl + 256, r[0]);
-            tmem_ld_32x32b_x32(tl + 256 + 32, r[1]);
-            tmem_wait_ld_r(r[0]);
-            tmem_wait_ld_r(r[1]);
+            tmem_ld_32x32b_x32(tl + 256 + kCols * e, r);
+            tmem_wait_ld_r(r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(m.d_read);
 #pragma unroll
-            for (int c = 0; c < 64; ++c) p[c] *= __uint_as_float(r[c >> 5][c & 31]) - delta;
-            const int see = end - j * kTile - 64 * half;     // columns that this row sees
-            if (see < 64) {
+            for (int c = 0; c < 32; ++c) p[c] *= __uint_as_float(r[c]) - delta;
+            const int see = end - j * kTile - kCols * e;     // columns that this row sees
+            if (see < kCols) {
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
+                for (int c = 0; c < 32; ++c)
                     if (c >= see) p[c] = 0.f;
             }
-            uint32_t w[32];
+            uint32_t w[16];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-            tmem_st_32x32b_x32(ts, w);
+            for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+            tmem_st_32x32b_x16(ts, w);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -419,7 +488,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (lane == 0) fail();
         } else {
             tc_fence_after();
-            store_row<T::HDP>(tl - 64 * half + 384, dq0 + static_cast<size_t>(row) * g.lddq, g.hd, i < g.nq, g.scale, half, 2);
+            store_row<T::HDP>(tl + 384, dq0 + static_cast<size_t>(row) * g.lddq, g.hd, i < g.nq, g.scale, e, kGroups);
         }
     }
 
@@ -440,16 +509,20 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
-    using P = BwdPlan<NB, TAIL>;
+    using P = BwdPlan<NB, TAIL, false>;
     using T = AttnTile<NB, TAIL>;
-    constexpr int NS = P::STAGES;
+    constexpr int N0 = P::S0, N1 = P::S1;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sb = smem_u32(smem);
-    const BwdBars m = bwd_bars<NS>(sb + P::BAR_OFF);
+    const BwdBars m = bwd_bars<N0, N1>(sb + P::BAR_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + P::TMEM_SLOT_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::ABORT_OFF);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (smem - smem_raw + P::USED > P::BYTES) {       // the base of dynamic shared memory is 1 KB aligned
+        if (threadIdx.x == 0 && g.err) atomicExch(g.err, 1);
+        return;
+    }
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int kt = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
     const int key0 = kt * kTile, off = g.nk - g.nq;
     const int qtiles = (g.nq + kTile - 1) / kTile;
@@ -469,13 +542,21 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
 
     if (threadIdx.x == 0) {
-        bwd_init<NS>(m);
+        bwd_init<N0, N1>(m);
         *abort_flag = 0;
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
         tma_prefetch_desc(&maps.d);
     }
+    for (int i = threadIdx.x; i < 2 * kTile; i += kThreadsB) {
+        // ones against -L (first operand) or against -D (second)
+        uint4* sel = reinterpret_cast<uint4*>(smem + P::SEL_OFF);
+        const int x = (i >> 2) & 1;
+        sel[2 * i + x] = i < kTile ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0) : make_uint4(0, 0x3F800000u, 0x3F803F80u, 0);
+        sel[2 * i + 1 - x] = make_uint4(0, 0, 0, 0);
+    }
+    fence_proxy_async_smem();
     if (warp == 1) {
         tmem_alloc(sb + P::TMEM_SLOT_OFF, 512);
         tmem_relinquish();
@@ -483,7 +564,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
     // only now: the next kernel's CTAs may allocate TMEM before they wait for
     // this grid, so every CTA of this one must hold its own first
     pdl_launch_dependents();
@@ -507,23 +588,23 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         }
         int qt = t0, h = hk * g.group;
         for (int i = 0; i < n; ++i) {
-            const int st = i % NS;
-            const uint32_t ph = (i / NS) & 1;
+            const int st = i % N0, sd = i % N1;
+            const uint32_t ph = (i / N0) & 1, pd = (i / N1) & 1;
             const bool raw = fix < kTile && qt == t1 - 1;
-            const uint32_t full0 = raw ? m.raw0 : m.full0 + 8 * st, full1 = raw ? m.raw1 : m.full1 + 8 * st;
+            const uint32_t full0 = raw ? m.raw0 : m.full0 + 8 * st, full1 = raw ? m.raw1 : m.full1 + 8 * sd;
             if (lane == 0) {
                 ok = mbar_wait(m.empty0 + 8 * st, ph ^ 1, abort_flag);
                 if (ok) {
                     mbar_arrive_expect_tx(full0, P::TILE + kStatBytes);
                     load_tile<NB, TAIL>(sb + P::R0_OFF + st * P::TILE, &maps.q, &maps.qt, h, qt * kTile, b, full0);
                     bulk_load(sb + P::STAT_OFF + st * kStatBytes,
-                              g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * 2 * kTile, kStatBytes, full0);
+                              g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16), kStatBytes, full0);
                     if (!raw) f0.add(st, ph);
-                    ok = mbar_wait(m.empty1 + 8 * st, ph ^ 1, abort_flag);
+                    ok = mbar_wait(m.empty1 + 8 * sd, pd ^ 1, abort_flag);
                     if (ok) {
                         mbar_arrive_expect_tx(full1, P::TILE);
-                        load_tile<NB, TAIL>(sb + P::R1_OFF + st * P::TILE, &maps.d, &maps.dt, h, qt * kTile, b, full1);
-                        if (!raw) f1.add(st, ph);
+                        load_tile<NB, TAIL>(sb + P::R1_OFF + sd * P::TILE, &maps.d, &maps.dt, h, qt * kTile, b, full1);
+                        if (!raw) f1.add(sd, pd);
                     } else if (raw) {
                         mbar_wait(m.raw0, raws & 1, nullptr);
                     }
@@ -536,11 +617,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 ok = __all_sync(0xFFFFFFFFu, a0 && a1);
                 if (!ok) break;
                 zero_rows<NB, TAIL>(smem + P::R0_OFF + st * P::TILE, fix, lane, 32);
-                zero_rows<NB, TAIL>(smem + P::R1_OFF + st * P::TILE, fix, lane, 32);
+                zero_rows<NB, TAIL>(smem + P::R1_OFF + sd * P::TILE, fix, lane, 32);
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(m.full0 + 8 * st);
-                    mbar_arrive(m.full1 + 8 * st);
+                    mbar_arrive(m.full1 + 8 * sd);
                 }
                 ++raws;
             }
@@ -554,123 +635,153 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (!ok) fail();
             if (*abort_flag) {
                 mbar_wait(m.a_full, 0, nullptr);
-                f0.drain<NS>(m.full0);
-                f1.drain<NS>(m.full1);
+                f0.drain<N0>(m.full0);
+                f1.drain<N1>(m.full1);
             }
         }
-    } else if (warp == 1 && lane == 0) {
-        // ---------------- MMA issuer
+    } else if (warp == 1) {
+        // ---------------- MMA issuer: the warp waits, one lane issues
+        const bool one = elect_one();
         const uint64_t k = sw128_kmajor_desc(sb + P::A0_OFF), ktl = sw32_desc(sb + P::A0_OFF + NB * T::BLK);
         const uint64_t v = sw128_kmajor_desc(sb + P::A1_OFF), vtl = sw32_desc(sb + P::A1_OFF + NB * T::BLK);
         const uint64_t q = sw128_kmajor_desc(sb + P::R0_OFF), qmn = sw128_mnmajor_desc(sb + P::R0_OFF, T::BLK);
         const uint64_t qtl = sw32_desc(sb + P::R0_OFF + NB * T::BLK);
         const uint64_t d = sw128_kmajor_desc(sb + P::R1_OFF), dmn = sw128_mnmajor_desc(sb + P::R1_OFF, T::BLK);
         const uint64_t dtl = sw32_desc(sb + P::R1_OFF + NB * T::BLK);
+        const uint64_t sel = sw32_desc(sb + P::SEL_OFF), stat = sw32_desc(sb + P::STAT_OFF);
         auto issue_s = [&](int i) -> bool {
-            const int st = i % NS;
-            if (!mbar_wait(m.full0 + 8 * st, (i / NS) & 1, abort_flag)) return false;
+            const int st = i % N0;
+            if (!warp_wait(m.full0 + 8 * st, (i / N0) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint32_t so = (st * P::TILE) >> 4;
-            mma_scores<NB, TAIL>(tmem, k, ktl, q + so, qtl + so);
-            tc_commit(m.s_full);
+            if (one) {
+                mma_scores<NB, TAIL>(tmem, k, ktl, q + so, qtl + so);
+                tc_mma_f16(tmem, sel, stat + ((st * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
+                tc_commit(m.s_full);
+            }
+            __syncwarp();
             return true;
         };
         auto issue_dp = [&](int i) -> bool {
-            const int st = i % NS;
-            if (!mbar_wait(m.full1 + 8 * st, (i / NS) & 1, abort_flag)) return false;
+            const int st = i % N1;
+            if (!warp_wait(m.full1 + 8 * st, (i / N1) & 1, abort_flag)) return false;
             tc_fence_after();
             const uint32_t so = (st * P::TILE) >> 4;
-            mma_scores<NB, TAIL>(tmem + 128, v, vtl, d + so, dtl + so);
-            tc_commit(m.d_full);
+            if (one) {
+                mma_scores<NB, TAIL>(tmem + 128, v, vtl, d + so, dtl + so);
+                // the statistics came with Q_i, which S_i has waited for
+                tc_mma_f16(tmem + 128, sel + (kStatBytes >> 4), stat + ((i % N0 * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
+                tc_commit(m.d_full);
+            }
+            __syncwarp();
             return true;
         };
-        bool ok = mbar_wait(m.a_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
+        bool ok = warp_wait(m.a_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
         for (int i = 0; ok && i < n; ++i) {
-            const int st = i % NS;
-            const uint32_t so = (st * P::TILE) >> 4;
-            if (!mbar_wait(m.e0, i & 1, abort_flag)) { ok = false; break; }
+            const int st = i % N0, sd = i % N1;
+            const uint32_t so = (st * P::TILE) >> 4, sdo = (sd * P::TILE) >> 4;
+            const bool more = i + 1 < n;
+            // S_{i+1} takes S_i's place once that is read; where P_i lies there, after dV_i
+            if (P::P_APART && more && !(warp_wait(m.s_read, i & 1, abort_flag) && issue_s(i + 1))) { ok = false; break; }
+            if (!warp_wait(m.e0, i & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            mma_accumulate<NB, TAIL>(tmem + 256, tmem, dmn + so, dtl + so, i == 0);
-            tc_commit(m.empty1 + 8 * st);
-            if (i + 1 < n && !issue_s(i + 1)) { ok = false; break; }
-            if (!mbar_wait(m.e1, i & 1, abort_flag)) { ok = false; break; }
+            if (one) {
+                mma_accumulate<NB, TAIL, P::P_APART ? kCols / 2 : kCols>(tmem + P::DV_COL, tmem + P::P_COL, dmn + sdo, dtl + sdo, i == 0);
+                tc_commit(m.empty1 + 8 * sd);
+            }
+            __syncwarp();
+            if (!P::P_APART && more && !issue_s(i + 1)) { ok = false; break; }
+            // likewise dP_{i+1}, dS_i and dK_i
+            if (P::DS_APART && more && !(warp_wait(m.d_read, i & 1, abort_flag) && issue_dp(i + 1))) { ok = false; break; }
+            if (!warp_wait(m.e1, i & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            mma_accumulate<NB, TAIL>(tmem + 384, tmem + 128, qmn + so, qtl + so, i == 0);
-            tc_commit(m.empty0 + 8 * st);
-            if (i + 1 < n && !issue_dp(i + 1)) { ok = false; break; }
+            if (one) {
+                mma_accumulate<NB, TAIL, P::DS_APART ? kCols / 2 : kCols>(tmem + P::DK_COL, tmem + P::DS_COL, qmn + so, qtl + so, i == 0);
+                tc_commit(m.empty0 + 8 * st);
+            }
+            __syncwarp();
+            if (!P::DS_APART && more && !issue_dp(i + 1)) { ok = false; break; }
         }
-        if (ok) tc_commit(m.done);
-        else fail();
-        if (*abort_flag) {
-            tc_commit(m.drain);
-            mbar_wait(m.drain, 0, nullptr);
+        if (one) {
+            if (ok) tc_commit(m.done);
+            else fail();
+            if (*abort_flag) {
+                tc_commit(m.drain);
+                mbar_wait(m.drain, 0, nullptr);
+            }
         }
+        __syncwarp();
     } else if (warp >= 4) {
         // ---------------- elementwise: thread = key, half of the query columns
-        const int half = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+        const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;    // group, TMEM lane
         const int key = key0 + row;
         const int begin = key < klen ? query_begin(key, off, g.causal_block) : 1 << 30;   // queries that see it: [begin, qlen)
-        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + 64 * half;
+        const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t ts = tl + kCols * e;
         bool ok = true;
         int qt = t0;
         for (int i = 0; i < n; ++i) {
-            const int st = i % NS;
-            const float* stat = reinterpret_cast<const float*>(smem + P::STAT_OFF + st * kStatBytes) + 64 * half;
-            const int lo = begin - (qt * kTile + 64 * half), hi = qlen - (qt * kTile + 64 * half);
-            const bool cut = __any_sync(0xFFFFFFFFu, lo > 0 || hi < 64);
+            const int lo = begin - (qt * kTile + kCols * e), hi = qlen - (qt * kTile + kCols * e);
+            const bool cut = __any_sync(0xFFFFFFFFu, lo > 0 || hi < kCols);
             if (++qt == t1) qt = t0;
-            bool got = mbar_wait(m.full0 + 8 * st, (i / NS) & 1, abort_flag) && mbar_wait(m.s_full, i & 1, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
+            if (!warp_wait(m.s_full, i & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            uint32_t r[2][32], w[32];
-            float p[64];
-            tmem_ld_32x32b_x32(tl, r[0]);
-            tmem_ld_32x32b_x32(tl + 32, r[1]);
-            tmem_wait_ld_r(r[0]);
-            tmem_wait_ld_r(r[1]);
-#pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 l = *reinterpret_cast<const float4*>(stat + c);
-                p[c + 0] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][(c + 0) & 31]), g.scale_log2, -l.x));
-                p[c + 1] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][(c + 1) & 31]), g.scale_log2, -l.y));
-                p[c + 2] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][(c + 2) & 31]), g.scale_log2, -l.z));
-                p[c + 3] = ex2_approx(fmaf(__uint_as_float(r[c >> 5][(c + 3) & 31]), g.scale_log2, -l.w));
+            uint32_t r[32], w[16];
+            float p[32];
+            tmem_ld_32x32b_x32(ts, r);
+            tmem_wait_ld_r(r);
+            if constexpr (P::P_APART) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m.s_read);
             }
+            // the product holds S - L
+#pragma unroll
+            for (int c = 0; c < 32; ++c) p[c] = ex2_approx(__uint_as_float(r[c]) * g.scale_log2);
             if (cut) {
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
+                for (int c = 0; c < 32; ++c)
                     if (c < lo || c >= hi) p[c] = 0.f;
             }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-            tmem_st_32x32b_x32(tl, w);
+            for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+            if constexpr (P::P_APART) {
+                // the last reader of its columns, dV_{i-1}, releases its dO stage when done
+                if (i > 0 && !warp_wait(m.empty1 + 8 * ((i - 1) % N1), ((i - 1) / N1) & 1, abort_flag)) { ok = false; break; }
+                tmem_st_32x32b_x16(tl + P::P_COL + kCols / 2 * e, w);
+            } else {
+                tmem_st_32x32b_x16(ts, w);
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(m.e0);
-            got = mbar_wait(m.d_full, i & 1, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
+            if (!warp_wait(m.d_full, i & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            tmem_ld_32x32b_x32(tl + 128, r[0]);
-            tmem_ld_32x32b_x32(tl + 128 + 32, r[1]);
-            tmem_wait_ld_r(r[0]);
-            tmem_wait_ld_r(r[1]);
-#pragma unroll
-            for (int c = 0; c < 64; c += 4) {
-                const float4 e = *reinterpret_cast<const float4*>(stat + kTile + c);
-                p[c + 0] *= __uint_as_float(r[c >> 5][(c + 0) & 31]) - e.x;
-                p[c + 1] *= __uint_as_float(r[c >> 5][(c + 1) & 31]) - e.y;
-                p[c + 2] *= __uint_as_float(r[c >> 5][(c + 2) & 31]) - e.z;
-                p[c + 3] *= __uint_as_float(r[c >> 5][(c + 3) & 31]) - e.w;
+            tmem_ld_32x32b_x32(ts + 128, r);
+            tmem_wait_ld_r(r);
+            if constexpr (P::DS_APART) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m.d_read);
             }
+            // this one dP - D
+#pragma unroll
+            for (int c = 0; c < 32; ++c) p[c] *= __uint_as_float(r[c]);
             if (cut) {
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
+                for (int c = 0; c < 32; ++c)
                     if (c < lo || c >= hi) p[c] = 0.f;
             }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-            tmem_st_32x32b_x32(tl + 128, w);
+            for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
+            if constexpr (P::DS_APART) {
+                // the last reader of its columns, dK_{i-1}, releases its Q stage when done
+                if (i > 0 && !warp_wait(m.empty0 + 8 * ((i - 1) % N0), ((i - 1) / N0) & 1, abort_flag)) { ok = false; break; }
+                tmem_st_32x32b_x16(tl + P::DS_COL + kCols / 2 * e, w);
+            } else {
+                tmem_st_32x32b_x16(ts + 128, w);
+            }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -681,9 +792,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (lane == 0) fail();
         } else {
             tc_fence_after();
-            const uint32_t acc = tl - 64 * half + 256 + 128 * half;
-            __nv_bfloat16* out = half ? dk0 + static_cast<size_t>(row) * g.lddk : dv0 + static_cast<size_t>(row) * g.lddv;
-            store_row<T::HDP>(acc, out, g.hd, key < g.nk, half ? g.scale : 1.f, 0, 1);
+            // even groups write dV, odd ones dK
+            const bool k = e & 1;
+            __nv_bfloat16* out = k ? dk0 + static_cast<size_t>(row) * g.lddk : dv0 + static_cast<size_t>(row) * g.lddv;
+            store_row<T::HDP>(tl + (k ? P::DK_COL : P::DV_COL), out, g.hd, key < g.nk, k ? g.scale : 1.f, e >> 1, kGroups / 2);
         }
     }
 
@@ -699,14 +811,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 template <int NB, bool TAIL>
 cudaError_t run_bwd(const BwdMaps& maps, const BwdArgs& g, int batch, int kv_heads, cudaStream_t s,
                     unsigned long long* launches) {
-    using P = BwdPlan<NB, TAIL>;
+    using PQ = BwdPlan<NB, TAIL, true>;
+    using PK = BwdPlan<NB, TAIL, false>;
     static unsigned long long set[2] = {0, 0};
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dq_kernel<NB, TAIL>), P::BYTES, &set[0]); e != cudaSuccess) return e;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dkv_kernel<NB, TAIL>), P::BYTES, &set[1]); e != cudaSuccess) return e;
-    cudaError_t e = launch_k(dq_kernel<NB, TAIL>, dim3((g.nq + kTile - 1) / kTile, g.heads, batch), kThreadsB, P::BYTES, s, maps, g);
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dq_kernel<NB, TAIL>), PQ::BYTES, &set[0]); e != cudaSuccess) return e;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dkv_kernel<NB, TAIL>), PK::BYTES, &set[1]); e != cudaSuccess) return e;
+    cudaError_t e = launch_k(dq_kernel<NB, TAIL>, dim3((g.nq + kTile - 1) / kTile, g.heads, batch), kThreadsB, PQ::BYTES, s, maps, g);
     ++*launches;
     if (e != cudaSuccess) return e;
-    e = launch_k(dkv_kernel<NB, TAIL>, dim3((g.nk + kTile - 1) / kTile, kv_heads, batch), kThreadsB, P::BYTES, s, maps, g);
+    e = launch_k(dkv_kernel<NB, TAIL>, dim3((g.nk + kTile - 1) / kTile, kv_heads, batch), kThreadsB, PK::BYTES, s, maps, g);
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -735,7 +848,7 @@ cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K
     g.O = static_cast<const __nv_bfloat16*>(O);
     g.dO = static_cast<const __nv_bfloat16*>(dO);
     g.lse = lse;
-    g.stats = static_cast<float*>(ws);
+    g.stats = static_cast<uint4*>(ws);
     g.dQ = static_cast<__nv_bfloat16*>(dQ);
     g.dK = static_cast<__nv_bfloat16*>(dK);
     g.dV = static_cast<__nv_bfloat16*>(dV);
