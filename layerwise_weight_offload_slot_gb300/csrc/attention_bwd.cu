@@ -67,15 +67,38 @@ struct BwdArgs {
 // rings that move (K and V; Q and dO), operand tiles for bf16 dS and P, and
 // per-row statistics.  DQ: the plan of dq_kernel.
 //
-// Ring depths: a tile of ring 0 is held from its first product to the last one
-// of the iteration, one of ring 1 shorter, and a reload takes ~1 us from L2.
-// Three and two stages hide it; dkv_kernel at head dims over 80 has room for
-// two and two.
+// A reload takes ~1 us (2000 cycles) from L2, longer than an iteration's
+// products.  Tile i of the first stream (K in dq_kernel, Q in dkv_kernel) is
+// held from its first product to the last one of its iteration, one of the
+// second (V, dO) for a shorter time.  Up to head dim 80 each stream has three
+// slots.  Above, the two streams share five (dq) or four (dkv) slots so that
+// the earlier freed tile makes room for the tile needed sooner: slot s holds
+// first-stream tile s, then second-stream tile s + SLOTS - 2, then first-stream
+// tile s + SLOTS, ... (slots 2.. begin with the second stream).  Against separate
+// 3 + 2 and 2 + 2 rings this leaves a reload 4/3 (dq) and 1 (dkv) iterations.
+struct Slot {
+    int s;
+    uint32_t ph;              // parity of this use of the slot's barriers
+};
+
+template <int SLOTS, bool SHARED, bool SECOND>
+__device__ __forceinline__ Slot slot_of(int i) {
+    if constexpr (SHARED) {
+        const int r = i % SLOTS;
+        return SECOND ? Slot{(i + 2) % SLOTS, r >= SLOTS - 2 ? 1u : 0u} : Slot{r, r >= 2 ? 1u : 0u};
+    } else {
+        constexpr int N = SLOTS / 2;
+        return {i % N + (SECOND ? N : 0), static_cast<uint32_t>(i / N) & 1u};
+    }
+}
+
 template <int NB, bool TAIL, bool DQ>
 struct BwdPlan {
     using T = AttnTile<NB, TAIL>;
     static constexpr int TILE = T::BYTES;
-    static constexpr int S0 = DQ || NB == 1 ? 3 : 2, S1 = 2;
+    static constexpr bool SHARED = NB == 2;
+    static constexpr int SLOTS = SHARED ? (DQ ? 5 : 4) : 6;
+    static constexpr int STATS = SHARED ? 2 : 3;            // statistics operands of dkv_kernel, tile i in i % STATS
     // dkv_kernel's tensor memory: S^T [0, 128), dP^T [128, 256), then dV and dK, then P^T
     // and dS^T (64 columns each) where 512 columns hold them.  A P or dS that
     // takes the place of its product instead makes the next product wait for it.
@@ -85,14 +108,13 @@ struct BwdPlan {
     static constexpr uint32_t P_COL = P_APART ? DK_COL + T::HDP : 0;
     static constexpr uint32_t DS_COL = DS_APART ? P_COL + 64 : 128;
     static constexpr int A0_OFF = 0, A1_OFF = TILE;
-    static constexpr int R0_OFF = 2 * TILE;
-    static constexpr int R1_OFF = R0_OFF + S0 * TILE;
-    // dq: partial sums of D; dkv: the two selecting operands, then statistics per ring-0 stage
-    static constexpr int SEL_OFF = R1_OFF + S1 * TILE;
+    static constexpr int R_OFF = 2 * TILE;
+    // dq: partial sums of D; dkv: the two selecting operands, then the statistics
+    static constexpr int SEL_OFF = R_OFF + SLOTS * TILE;
     static constexpr int STAT_OFF = SEL_OFF + 2 * kStatBytes;
-    static constexpr int BAR_OFF = DQ ? SEL_OFF + kGroups * kTile * 4 : STAT_OFF + S0 * kStatBytes;
-    // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, s_read, d_read; full0, empty0 [S0]; full1, empty1 [S1]
-    static constexpr int NBARS = 12 + 2 * S0 + 2 * S1;
+    static constexpr int BAR_OFF = DQ ? SEL_OFF + kGroups * kTile * 4 : STAT_OFF + STATS * kStatBytes;
+    // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, s_read, d_read; full, empty [SLOTS]
+    static constexpr int NBARS = 12 + 2 * SLOTS;
     static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
     static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
     static constexpr int USED = ABORT_OFF + 4;
@@ -105,16 +127,16 @@ struct BwdPlan {
 };
 
 struct BwdBars {
-    uint32_t a_full, raw0, raw1, s_full, d_full, e0, e1, done, drain, s_read, d_read, full0, empty0, full1, empty1;
+    uint32_t a_full, raw0, raw1, s_full, d_full, e0, e1, done, drain, s_read, d_read, full, empty;
 };
 
-template <int S0, int S1>
+template <int SLOTS>
 __device__ __forceinline__ BwdBars bwd_bars(uint32_t b) {
     return {b, b + 8, b + 16, b + 24, b + 40, b + 48, b + 56, b + 64, b + 72, b + 80, b + 88,
-            b + 96, b + 96 + 8 * S0, b + 96 + 16 * S0, b + 96 + 16 * S0 + 8 * S1};
+            b + 96, b + 96 + 8 * SLOTS};
 }
 
-template <int S0, int S1>
+template <int SLOTS>
 __device__ __forceinline__ void bwd_init(const BwdBars& m) {
     mbar_init(m.a_full, 1);
     mbar_init(m.raw0, 1);
@@ -128,13 +150,9 @@ __device__ __forceinline__ void bwd_init(const BwdBars& m) {
     mbar_init(m.d_read, 4 * kGroups);
     mbar_init(m.done, 1);
     mbar_init(m.drain, 1);
-    for (int i = 0; i < S0; ++i) {
-        mbar_init(m.full0 + 8 * i, 1);
-        mbar_init(m.empty0 + 8 * i, 1);
-    }
-    for (int i = 0; i < S1; ++i) {
-        mbar_init(m.full1 + 8 * i, 1);
-        mbar_init(m.empty1 + 8 * i, 1);
+    for (int i = 0; i < SLOTS; ++i) {
+        mbar_init(m.full + 8 * i, 1);
+        mbar_init(m.empty + 8 * i, 1);
     }
     fence_mbar_init();
 }
@@ -144,16 +162,16 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
 
-// Loads of a ring in flight, for the drain: stages and the parity of each.
+// Loads in flight, for the drain: slots and the parity of each.
 struct InFlight {
     uint32_t on = 0, par = 0;
-    __device__ void add(int st, uint32_t ph) {
-        on |= 1u << st;
-        par = (par & ~(1u << st)) | (ph << st);
+    __device__ void add(Slot s) {
+        on |= 1u << s.s;
+        par = (par & ~(1u << s.s)) | (s.ph << s.s);
     }
-    template <int STAGES>
+    template <int SLOTS>
     __device__ void drain(uint32_t full) const {
-        for (int i = 0; i < STAGES; ++i)
+        for (int i = 0; i < SLOTS; ++i)
             if (on & (1u << i)) mbar_wait(full + 8 * i, (par >> i) & 1u, nullptr);
     }
 };
@@ -259,11 +277,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
     using P = BwdPlan<NB, TAIL, true>;
     using T = AttnTile<NB, TAIL>;
-    constexpr int N0 = P::S0, N1 = P::S1;
+    const auto first = [](int i) { return slot_of<P::SLOTS, P::SHARED, false>(i); };
+    const auto second = [](int i) { return slot_of<P::SLOTS, P::SHARED, true>(i); };
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sb = smem_u32(smem);
-    const BwdBars m = bwd_bars<N0, N1>(sb + P::BAR_OFF);
+    const BwdBars m = bwd_bars<P::SLOTS>(sb + P::BAR_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + P::TMEM_SLOT_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::ABORT_OFF);
     if (smem - smem_raw + P::USED > P::BYTES) {       // the base of dynamic shared memory is 1 KB aligned
@@ -288,7 +307,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
 
     if (threadIdx.x == 0) {
-        bwd_init<N0, N1>(m);
+        bwd_init<P::SLOTS>(m);
         *abort_flag = 0;
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
@@ -311,53 +330,51 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (g.err) atomicExch(g.err, 1);
     };
     // keys behind k_lens end inside the last tile: its K rows there become zero
-    // before the MMAs see it (its loads complete on raw0 instead of full0)
+    // before the MMAs see it (its loads complete on raw0 instead)
     const int fix = klen < g.nk && klen < n * kTile ? klen - (n - 1) * kTile : kTile;
 
     if (warp == 0) {
-        // ---------------- TMA: ring 0 holds K, ring 1 V
+        // ---------------- TMA: K and V
         bool ok = true;
-        InFlight f0, f1;
+        InFlight in;
         if (lane == 0) {
             const int hk = h / g.group;
             mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
             load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, row0, b, m.a_full);
             load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, row0, b, m.a_full);
             for (int j = 0; j < n; ++j) {
-                const int st = j % N0, sv = j % N1;
-                const uint32_t ph = (j / N0) & 1, pv = (j / N1) & 1;
-                if (!mbar_wait(m.empty0 + 8 * st, ph ^ 1, abort_flag)) { ok = false; break; }
+                const Slot k = first(j), v = second(j);
+                if (!mbar_wait(m.empty + 8 * k.s, k.ph ^ 1, abort_flag)) { ok = false; break; }
                 const bool raw = fix < kTile && j == n - 1;
-                const uint32_t full = raw ? m.raw0 : m.full0 + 8 * st;
+                const uint32_t full = raw ? m.raw0 : m.full + 8 * k.s;
                 mbar_arrive_expect_tx(full, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R0_OFF + st * P::TILE, &maps.k, &maps.kt, hk, j * kTile, b, full);
-                if (!raw) f0.add(st, ph);
-                if (!mbar_wait(m.empty1 + 8 * sv, pv ^ 1, abort_flag)) {
+                load_tile<NB, TAIL>(sb + P::R_OFF + k.s * P::TILE, &maps.k, &maps.kt, hk, j * kTile, b, full);
+                if (!raw) in.add(k);
+                if (!mbar_wait(m.empty + 8 * v.s, v.ph ^ 1, abort_flag)) {
                     ok = false;
                     if (raw) mbar_wait(m.raw0, 0, nullptr);
                     break;
                 }
-                mbar_arrive_expect_tx(m.full1 + 8 * sv, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R1_OFF + sv * P::TILE, &maps.v, &maps.vt, hk, j * kTile, b, m.full1 + 8 * sv);
-                f1.add(sv, pv);
+                mbar_arrive_expect_tx(m.full + 8 * v.s, P::TILE);
+                load_tile<NB, TAIL>(sb + P::R_OFF + v.s * P::TILE, &maps.v, &maps.vt, hk, j * kTile, b, m.full + 8 * v.s);
+                in.add(v);
             }
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
         if (ok && fix < kTile) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(m.raw0, 0, nullptr));
             if (ok) {
-                const int st = (n - 1) % N0;
-                zero_rows<NB, TAIL>(smem + P::R0_OFF + st * P::TILE, fix, lane, 32);
+                const int st = first(n - 1).s;
+                zero_rows<NB, TAIL>(smem + P::R_OFF + st * P::TILE, fix, lane, 32);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(m.full0 + 8 * st);
+                if (lane == 0) mbar_arrive(m.full + 8 * st);
             }
         }
         if (lane == 0) {
             if (!ok) fail();
             if (*abort_flag) {
                 mbar_wait(m.a_full, 0, nullptr);
-                f0.drain<N0>(m.full0);
-                f1.drain<N1>(m.full1);
+                in.drain<P::SLOTS>(m.full);
             }
         }
     } else if (warp == 1) {
@@ -365,14 +382,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const bool one = elect_one();
         const uint64_t q = sw128_kmajor_desc(sb + P::A0_OFF), qtl = sw32_desc(sb + P::A0_OFF + NB * T::BLK);
         const uint64_t d = sw128_kmajor_desc(sb + P::A1_OFF), dtl = sw32_desc(sb + P::A1_OFF + NB * T::BLK);
-        const uint64_t k = sw128_kmajor_desc(sb + P::R0_OFF), kmn = sw128_mnmajor_desc(sb + P::R0_OFF, T::BLK);
-        const uint64_t ktl = sw32_desc(sb + P::R0_OFF + NB * T::BLK);
-        const uint64_t v = sw128_kmajor_desc(sb + P::R1_OFF), vtl = sw32_desc(sb + P::R1_OFF + NB * T::BLK);
+        const uint64_t k = sw128_kmajor_desc(sb + P::R_OFF), kmn = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK);
+        const uint64_t ktl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
+        const uint64_t v = sw128_kmajor_desc(sb + P::R_OFF), vtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
         auto issue_s = [&](int j) -> bool {
-            const int st = j % N0;
-            if (!warp_wait(m.full0 + 8 * st, (j / N0) & 1, abort_flag)) return false;
+            const Slot t = first(j);
+            if (!warp_wait(m.full + 8 * t.s, t.ph, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t so = (st * P::TILE) >> 4;
+            const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
                 mma_scores<NB, TAIL>(tmem + (j & 1) * 128, q, qtl, k + so, ktl + so);
                 tc_commit(m.s_full + 8 * (j & 1));
@@ -381,14 +398,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             return true;
         };
         auto issue_dp = [&](int j) -> bool {
-            const int st = j % N1;
-            if (!warp_wait(m.full1 + 8 * st, (j / N1) & 1, abort_flag)) return false;
+            const Slot t = second(j);
+            if (!warp_wait(m.full + 8 * t.s, t.ph, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t so = (st * P::TILE) >> 4;
+            const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
                 mma_scores<NB, TAIL>(tmem + 256, d, dtl, v + so, vtl + so);
                 tc_commit(m.d_full);
-                tc_commit(m.empty1 + 8 * st);
+                tc_commit(m.empty + 8 * t.s);
             }
             __syncwarp();
             return true;
@@ -402,11 +419,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
             if (!warp_wait(m.e0, j & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const int st = j % N0;
+            const int st = first(j).s;
             const uint32_t so = (st * P::TILE) >> 4;
             if (one) {
                 mma_accumulate<NB, TAIL, kCols>(tmem + 384, tmem + (j & 1) * 128, kmn + so, ktl + so, j == 0);
-                tc_commit(m.empty0 + 8 * st);
+                tc_commit(m.empty + 8 * st);
             }
             __syncwarp();
         }
@@ -511,11 +528,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
     using P = BwdPlan<NB, TAIL, false>;
     using T = AttnTile<NB, TAIL>;
-    constexpr int N0 = P::S0, N1 = P::S1;
+    const auto first = [](int i) { return slot_of<P::SLOTS, P::SHARED, false>(i); };
+    const auto second = [](int i) { return slot_of<P::SLOTS, P::SHARED, true>(i); };
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t sb = smem_u32(smem);
-    const BwdBars m = bwd_bars<N0, N1>(sb + P::BAR_OFF);
+    const BwdBars m = bwd_bars<P::SLOTS>(sb + P::BAR_OFF);
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + P::TMEM_SLOT_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::ABORT_OFF);
     if (smem - smem_raw + P::USED > P::BYTES) {       // the base of dynamic shared memory is 1 KB aligned
@@ -542,7 +560,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
 
     if (threadIdx.x == 0) {
-        bwd_init<N0, N1>(m);
+        bwd_init<P::SLOTS>(m);
         *abort_flag = 0;
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
@@ -577,9 +595,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int fix = qlen < g.nq && qlen < t1 * kTile ? qlen - (t1 - 1) * kTile : kTile;
 
     if (warp == 0) {
-        // ---------------- TMA: ring 0 holds Q and the row statistics, ring 1 dO
+        // ---------------- TMA: Q with the row statistics, and dO
         bool ok = true;
-        InFlight f0, f1;
+        InFlight in;
         uint32_t raws = 0;        // tiles fixed so far
         if (lane == 0) {
             mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
@@ -588,23 +606,22 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         }
         int qt = t0, h = hk * g.group;
         for (int i = 0; i < n; ++i) {
-            const int st = i % N0, sd = i % N1;
-            const uint32_t ph = (i / N0) & 1, pd = (i / N1) & 1;
+            const Slot q = first(i), d = second(i);
             const bool raw = fix < kTile && qt == t1 - 1;
-            const uint32_t full0 = raw ? m.raw0 : m.full0 + 8 * st, full1 = raw ? m.raw1 : m.full1 + 8 * sd;
+            const uint32_t full0 = raw ? m.raw0 : m.full + 8 * q.s, full1 = raw ? m.raw1 : m.full + 8 * d.s;
             if (lane == 0) {
-                ok = mbar_wait(m.empty0 + 8 * st, ph ^ 1, abort_flag);
+                ok = mbar_wait(m.empty + 8 * q.s, q.ph ^ 1, abort_flag);
                 if (ok) {
                     mbar_arrive_expect_tx(full0, P::TILE + kStatBytes);
-                    load_tile<NB, TAIL>(sb + P::R0_OFF + st * P::TILE, &maps.q, &maps.qt, h, qt * kTile, b, full0);
-                    bulk_load(sb + P::STAT_OFF + st * kStatBytes,
+                    load_tile<NB, TAIL>(sb + P::R_OFF + q.s * P::TILE, &maps.q, &maps.qt, h, qt * kTile, b, full0);
+                    bulk_load(sb + P::STAT_OFF + i % P::STATS * kStatBytes,
                               g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16), kStatBytes, full0);
-                    if (!raw) f0.add(st, ph);
-                    ok = mbar_wait(m.empty1 + 8 * sd, pd ^ 1, abort_flag);
+                    if (!raw) in.add(q);
+                    ok = mbar_wait(m.empty + 8 * d.s, d.ph ^ 1, abort_flag);
                     if (ok) {
                         mbar_arrive_expect_tx(full1, P::TILE);
-                        load_tile<NB, TAIL>(sb + P::R1_OFF + sd * P::TILE, &maps.d, &maps.dt, h, qt * kTile, b, full1);
-                        if (!raw) f1.add(sd, pd);
+                        load_tile<NB, TAIL>(sb + P::R_OFF + d.s * P::TILE, &maps.d, &maps.dt, h, qt * kTile, b, full1);
+                        if (!raw) in.add(d);
                     } else if (raw) {
                         mbar_wait(m.raw0, raws & 1, nullptr);
                     }
@@ -616,12 +633,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 const bool a0 = mbar_wait(m.raw0, raws & 1, nullptr), a1 = mbar_wait(m.raw1, raws & 1, nullptr);
                 ok = __all_sync(0xFFFFFFFFu, a0 && a1);
                 if (!ok) break;
-                zero_rows<NB, TAIL>(smem + P::R0_OFF + st * P::TILE, fix, lane, 32);
-                zero_rows<NB, TAIL>(smem + P::R1_OFF + sd * P::TILE, fix, lane, 32);
+                zero_rows<NB, TAIL>(smem + P::R_OFF + q.s * P::TILE, fix, lane, 32);
+                zero_rows<NB, TAIL>(smem + P::R_OFF + d.s * P::TILE, fix, lane, 32);
                 __syncwarp();
                 if (lane == 0) {
-                    mbar_arrive(m.full0 + 8 * st);
-                    mbar_arrive(m.full1 + 8 * sd);
+                    mbar_arrive(m.full + 8 * q.s);
+                    mbar_arrive(m.full + 8 * d.s);
                 }
                 ++raws;
             }
@@ -635,8 +652,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (!ok) fail();
             if (*abort_flag) {
                 mbar_wait(m.a_full, 0, nullptr);
-                f0.drain<N0>(m.full0);
-                f1.drain<N1>(m.full1);
+                in.drain<P::SLOTS>(m.full);
             }
         }
     } else if (warp == 1) {
@@ -644,33 +660,33 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const bool one = elect_one();
         const uint64_t k = sw128_kmajor_desc(sb + P::A0_OFF), ktl = sw32_desc(sb + P::A0_OFF + NB * T::BLK);
         const uint64_t v = sw128_kmajor_desc(sb + P::A1_OFF), vtl = sw32_desc(sb + P::A1_OFF + NB * T::BLK);
-        const uint64_t q = sw128_kmajor_desc(sb + P::R0_OFF), qmn = sw128_mnmajor_desc(sb + P::R0_OFF, T::BLK);
-        const uint64_t qtl = sw32_desc(sb + P::R0_OFF + NB * T::BLK);
-        const uint64_t d = sw128_kmajor_desc(sb + P::R1_OFF), dmn = sw128_mnmajor_desc(sb + P::R1_OFF, T::BLK);
-        const uint64_t dtl = sw32_desc(sb + P::R1_OFF + NB * T::BLK);
+        const uint64_t q = sw128_kmajor_desc(sb + P::R_OFF), qmn = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK);
+        const uint64_t qtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
+        const uint64_t d = sw128_kmajor_desc(sb + P::R_OFF), dmn = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK);
+        const uint64_t dtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
         const uint64_t sel = sw32_desc(sb + P::SEL_OFF), stat = sw32_desc(sb + P::STAT_OFF);
         auto issue_s = [&](int i) -> bool {
-            const int st = i % N0;
-            if (!warp_wait(m.full0 + 8 * st, (i / N0) & 1, abort_flag)) return false;
+            const Slot t = first(i);
+            if (!warp_wait(m.full + 8 * t.s, t.ph, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t so = (st * P::TILE) >> 4;
+            const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
                 mma_scores<NB, TAIL>(tmem, k, ktl, q + so, qtl + so);
-                tc_mma_f16(tmem, sel, stat + ((st * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
+                tc_mma_f16(tmem, sel, stat + ((i % P::STATS * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
                 tc_commit(m.s_full);
             }
             __syncwarp();
             return true;
         };
         auto issue_dp = [&](int i) -> bool {
-            const int st = i % N1;
-            if (!warp_wait(m.full1 + 8 * st, (i / N1) & 1, abort_flag)) return false;
+            const Slot t = second(i);
+            if (!warp_wait(m.full + 8 * t.s, t.ph, abort_flag)) return false;
             tc_fence_after();
-            const uint32_t so = (st * P::TILE) >> 4;
+            const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
                 mma_scores<NB, TAIL>(tmem + 128, v, vtl, d + so, dtl + so);
                 // the statistics came with Q_i, which S_i has waited for
-                tc_mma_f16(tmem + 128, sel + (kStatBytes >> 4), stat + ((i % N0 * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
+                tc_mma_f16(tmem + 128, sel + (kStatBytes >> 4), stat + ((i % P::STATS * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
                 tc_commit(m.d_full);
             }
             __syncwarp();
@@ -678,7 +694,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         };
         bool ok = warp_wait(m.a_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
         for (int i = 0; ok && i < n; ++i) {
-            const int st = i % N0, sd = i % N1;
+            const int st = first(i).s, sd = second(i).s;
             const uint32_t so = (st * P::TILE) >> 4, sdo = (sd * P::TILE) >> 4;
             const bool more = i + 1 < n;
             // S_{i+1} takes S_i's place once that is read; where P_i lies there, after dV_i
@@ -687,7 +703,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             if (one) {
                 mma_accumulate<NB, TAIL, P::P_APART ? kCols / 2 : kCols>(tmem + P::DV_COL, tmem + P::P_COL, dmn + sdo, dtl + sdo, i == 0);
-                tc_commit(m.empty1 + 8 * sd);
+                tc_commit(m.empty + 8 * sd);
             }
             __syncwarp();
             if (!P::P_APART && more && !issue_s(i + 1)) { ok = false; break; }
@@ -697,7 +713,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             if (one) {
                 mma_accumulate<NB, TAIL, P::DS_APART ? kCols / 2 : kCols>(tmem + P::DK_COL, tmem + P::DS_COL, qmn + so, qtl + so, i == 0);
-                tc_commit(m.empty0 + 8 * st);
+                tc_commit(m.empty + 8 * st);
             }
             __syncwarp();
             if (!P::DS_APART && more && !issue_dp(i + 1)) { ok = false; break; }
@@ -746,8 +762,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
             for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
             if constexpr (P::P_APART) {
-                // the last reader of its columns, dV_{i-1}, releases its dO stage when done
-                if (i > 0 && !warp_wait(m.empty1 + 8 * ((i - 1) % N1), ((i - 1) / N1) & 1, abort_flag)) { ok = false; break; }
+                // the last reader of its columns, dV_{i-1}, releases its dO slot when done
+                const Slot t = second(i - 1);
+                if (i > 0 && !warp_wait(m.empty + 8 * t.s, t.ph, abort_flag)) { ok = false; break; }
                 tmem_st_32x32b_x16(tl + P::P_COL + kCols / 2 * e, w);
             } else {
                 tmem_st_32x32b_x16(ts, w);
@@ -776,8 +793,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
             for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
             if constexpr (P::DS_APART) {
-                // the last reader of its columns, dK_{i-1}, releases its Q stage when done
-                if (i > 0 && !warp_wait(m.empty0 + 8 * ((i - 1) % N0), ((i - 1) / N0) & 1, abort_flag)) { ok = false; break; }
+                // the last reader of its columns, dK_{i-1}, releases its Q slot when done
+                const Slot t = first(i - 1);
+                if (i > 0 && !warp_wait(m.empty + 8 * t.s, t.ph, abort_flag)) { ok = false; break; }
                 tmem_st_32x32b_x16(tl + P::DS_COL + kCols / 2 * e, w);
             } else {
                 tmem_st_32x32b_x16(ts + 128, w);
