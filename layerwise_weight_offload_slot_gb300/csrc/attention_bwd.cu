@@ -306,6 +306,27 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         return;
     }
 
+    // D = rowsum(dO O) of row (threadIdx.x % 128), each group a part of the
+    // columns, all loads at once: they overlap the set-up
+    float* part = reinterpret_cast<float*>(smem + P::SEL_OFF);
+    float l2 = INFINITY;                // L in units of log2
+    if (warp >= 4) {
+        const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, i = row0 + row;
+        uint4 o[4], d[4];
+        float l = -INFINITY, t = 0.f;
+        if (i < qlen) l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int c = e + kGroups * u;
+            const bool in = i < qlen && c < g.hd / 8;
+            o[u] = in ? reinterpret_cast<const uint4*>(g.O + (static_cast<size_t>(b) * g.nq + i) * g.ldo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
+            d[u] = in ? reinterpret_cast<const uint4*>(g.dO + (static_cast<size_t>(b) * g.nq + i) * g.lddo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) t += dot8(o[u], d[u]);
+        part[e * kTile + row] = t;
+        if (l != -INFINITY) l2 = l * 1.4426950408889634f;
+    }
     if (threadIdx.x == 0) {
         bwd_init<P::SLOTS>(m);
         *abort_flag = 0;
@@ -440,43 +461,30 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         // ---------------- elementwise: thread = query row, half of the columns
         const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;    // group, TMEM lane
         const int i = row0 + row;
-        const bool valid = i < qlen;
-        const int end = valid ? key_end(i, off, g.causal_block, klen) : 0;
-        // D = rowsum(dO O): each group adds a part of the columns
-        float* part = reinterpret_cast<float*>(smem + P::SEL_OFF);
+        const int end = i < qlen ? key_end(i, off, g.causal_block, klen) : 0;
         float delta = 0.f;
-        if (valid) {
-            const uint4* o = reinterpret_cast<const uint4*>(g.O + (static_cast<size_t>(b) * g.nq + i) * g.ldo + h * g.hd);
-            const uint4* d = reinterpret_cast<const uint4*>(g.dO + (static_cast<size_t>(b) * g.nq + i) * g.lddo + h * g.hd);
-            for (int c = e; c < g.hd / 8; c += kGroups) delta += dot8(o[c], d[c]);
-        }
-        part[e * kTile + row] = delta;
-        asm volatile("bar.sync 1, %0;" ::"n"(kThreadsB - 128) : "memory");
-        delta = 0.f;
 #pragma unroll
         for (int c = 0; c < kGroups; ++c) delta += part[c * kTile + row];
-        float l2 = INFINITY;
-        if (valid) {
-            const float l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
-            if (l != -INFINITY) l2 = l * 1.4426950408889634f;
-        }
         // -L in units of the raw score
         if (e == 0) write_stat(stat, row, l2 == INFINITY ? kNothing : -l2 / g.scale_log2, -delta);
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint64_t scale2 = f32x2(g.scale_log2, g.scale_log2), neg_l2 = f32x2(-l2, -l2), neg_d = f32x2(-delta, -delta);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
             const uint32_t ts = tl + (j & 1) * 128 + kCols * e;
-            bool got = mbar_wait(m.s_full + 8 * (j & 1), (j >> 1) & 1, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
+            if (!warp_wait(m.s_full + 8 * (j & 1), (j >> 1) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             uint32_t r[32];
             tmem_ld_32x32b_x32(ts, r);
             tmem_wait_ld_r(r);
             float p[32];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) p[c] = ex2_approx(fmaf(__uint_as_float(r[c]), g.scale_log2, -l2));
-            got = mbar_wait(m.d_full, j & 1, abort_flag);
-            if (!__all_sync(0xFFFFFFFFu, got)) { ok = false; break; }
+            for (int c = 0; c < 32; c += 2) {
+                f32x2_split(fma_f32x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2, neg_l2), p[c], p[c + 1]);
+                p[c] = ex2_approx(p[c]);
+                p[c + 1] = ex2_approx(p[c + 1]);
+            }
+            if (!warp_wait(m.d_full, j & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             tmem_ld_32x32b_x32(tl + 256 + kCols * e, r);
             tmem_wait_ld_r(r);
@@ -484,7 +492,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(m.d_read);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) p[c] *= __uint_as_float(r[c]) - delta;
+            for (int c = 0; c < 32; c += 2)
+                f32x2_split(mul_f32x2(f32x2(p[c], p[c + 1]), add_f32x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), neg_d)),
+                            p[c], p[c + 1]);
             const int see = end - j * kTile - kCols * e;     // columns that this row sees
             if (see < kCols) {
 #pragma unroll
@@ -734,6 +744,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const int begin = key < klen ? query_begin(key, off, g.causal_block) : 1 << 30;   // queries that see it: [begin, qlen)
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t ts = tl + kCols * e;
+        const uint64_t scale2 = f32x2(g.scale_log2, g.scale_log2);
         bool ok = true;
         int qt = t0;
         for (int i = 0; i < n; ++i) {
@@ -753,7 +764,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
             // the product holds S - L
 #pragma unroll
-            for (int c = 0; c < 32; ++c) p[c] = ex2_approx(__uint_as_float(r[c]) * g.scale_log2);
+            for (int c = 0; c < 32; c += 2) {
+                f32x2_split(mul_f32x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), scale2), p[c], p[c + 1]);
+                p[c] = ex2_approx(p[c]);
+                p[c + 1] = ex2_approx(p[c + 1]);
+            }
             if (cut) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
@@ -784,7 +799,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
             // this one dP - D
 #pragma unroll
-            for (int c = 0; c < 32; ++c) p[c] *= __uint_as_float(r[c]);
+            for (int c = 0; c < 32; c += 2)
+                f32x2_split(mul_f32x2(f32x2(p[c], p[c + 1]), f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1]))), p[c], p[c + 1]);
             if (cut) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
