@@ -215,21 +215,36 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[j][k] = 0.f;
     }
-    int turn = 0;
-    for (int r = blockIdx.x * R; r < rows; r += parts * R, turn ^= 1) {
+    // the next row's pieces are on their way while this one's are used
+    uint4 xn[V8], dn[V8];
+    float rn = 0.f;
+    const auto load = [&](int r) {
         const bool live = r + rg < rows;
-        const size_t row = live ? r + rg : r;
+        const size_t row = live ? r + rg : 0;
         const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
         const uint4* dyr = reinterpret_cast<const uint4*>(dy + row * lddy);
-        uint4 xv[V8], dv[V8];
 #pragma unroll
         for (int j = 0; j < V8; ++j) {
             const int i = t0 + 32 * W * j;
             const bool in = live && i < n8;
-            xv[j] = in ? xr[i] : make_uint4(0, 0, 0, 0);
-            dv[j] = in ? dyr[i] : make_uint4(0, 0, 0, 0);
+            xn[j] = in ? xr[i] : make_uint4(0, 0, 0, 0);
+            dn[j] = in ? dyr[i] : make_uint4(0, 0, 0, 0);
         }
-        const float rs = rstd[row];
+        rn = live ? rstd[row] : 0.f;
+    };
+    load(blockIdx.x * R);
+    int turn = 0;
+    for (int r = blockIdx.x * R; r < rows; r += parts * R, turn ^= 1) {
+        const bool live = r + rg < rows;
+        const size_t row = live ? r + rg : r;
+        uint4 xv[V8], dv[V8];
+#pragma unroll
+        for (int j = 0; j < V8; ++j) {
+            xv[j] = xn[j];
+            dv[j] = dn[j];
+        }
+        const float rs = rn;
+        load(r + parts * R);
         float c = 0.f, unused = 0.f;
 #pragma unroll
         for (int j = 0; j < V8; ++j) {
@@ -293,11 +308,13 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
 
 // Adds `parts` partial rows per batch: out[b * out_ld + c] = sum over p of
 // part[((b * parts + p) * 2 + which) * D + c] (LayerNorm, both sums) or of one
-// row (RMSNorm, nsum = 1).  A CTA owns 32 float4 columns; its 8 warps add
-// every eighth partial row, then the 8 sums are added in order.
-__global__ void __launch_bounds__(256) column_sums_kernel(const float* __restrict__ part, int parts, int n4, int nsum,
-                                                          float* out1, float* out2, size_t out_ld) {
-    __shared__ float4 sh[8][32];
+// row (RMSNorm, nsum = 1).  A CTA owns 32 float4 columns; its 32 warps add
+// every 32nd partial row (at most 10, all loads in flight at once), then the
+// 32 sums are added in order, eight by eight.  Few columns make few CTAs, so
+// latency bounds it: 8 warps, 38 rows each, took 14.5 us for 304 x 5120.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restrict__ part, int parts, int n4, int nsum,
+                                                           float* out1, float* out2, size_t out_ld) {
+    __shared__ float4 sh[32][32];
     pdl_wait();
     pdl_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -305,24 +322,26 @@ __global__ void __launch_bounds__(256) column_sums_kernel(const float* __restric
     const int tile = blockIdx.x % tiles, rest = blockIdx.x / tiles;
     const int which = rest % nsum, b = rest / nsum;
     const int i = tile * 32 + lane;
+    const auto add = [](float4 a, float4 u) { return make_float4(a.x + u.x, a.y + u.y, a.z + u.z, a.w + u.w); };
     float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
     if (i < n4) {
         const float4* p = reinterpret_cast<const float4*>(part) + (static_cast<size_t>(b) * parts * nsum + which) * n4 + i;
-#pragma unroll 8
-        for (int k = warp; k < parts; k += 8) {
-            const float4 u = p[static_cast<size_t>(k) * nsum * n4];
-            t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
-        }
+#pragma unroll 10
+        for (int k = warp; k < parts; k += 32) t = add(t, p[static_cast<size_t>(k) * nsum * n4]);
     }
     sh[warp][lane] = t;
     __syncthreads();
-    if (warp == 0 && i < n4) {
-        t = sh[0][lane];
+    if (warp < 4) {
+        t = sh[8 * warp][lane];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) {
-            const float4 u = sh[k][lane];
-            t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
-        }
+        for (int k = 1; k < 8; ++k) t = add(t, sh[8 * warp + k][lane]);
+    }
+    __syncthreads();
+    if (warp < 4) sh[warp][lane] = t;
+    __syncthreads();
+    if (warp == 0 && i < n4) {
+#pragma unroll
+        for (int k = 1; k < 4; ++k) t = add(t, sh[k][lane]);
         reinterpret_cast<float4*>((which ? out2 : out1) + b * out_ld)[i] = t;
     }
 }
@@ -380,16 +399,16 @@ __global__ void __launch_bounds__(256)
 }
 
 // How the rows of one batch are spread: warps per row (w) and per CTA, CTAs
-// per batch (parts).  `vecs`: 16- or 8-byte pieces of a row, five a thread.
+// per batch (parts).  A row has `vecs` pieces, at most `each` a thread.
 struct NormPlan {
     int w, warps, parts;
     long long batches;
 };
 
-NormPlan norm_plan(int vecs, int rows, int rpb) {
+NormPlan norm_plan(int vecs, int each, int rows, int rpb) {
     NormPlan p;
     p.w = 1;
-    while (p.w < 32 && vecs > 5 * 32 * p.w) p.w *= 2;
+    while (p.w < 32 && vecs > each * 32 * p.w) p.w *= 2;
     p.warps = p.w <= 8 ? 8 : p.w;
     p.batches = (static_cast<long long>(rows) + rpb - 1) / rpb;
     const int per_sm = p.warps >= 32 ? 1 : 16 / p.warps;
@@ -412,7 +431,7 @@ size_t layernorm_bwd_workspace(int rows, int D, int rpb) {
     // of the two forms: column sums per batch, or over all rows
     size_t most = 256;
     for (int form = 0; form < 2; ++form) {
-        const NormPlan p = norm_plan(D / 4, rows, form ? rows : (rpb < rows ? rpb : rows));
+        const NormPlan p = norm_plan(D / 4, 5, rows, form ? rows : (rpb < rows ? rpb : rows));
         if (p.parts == 1) continue;
         const size_t n = static_cast<size_t>(p.batches) * p.parts * 2 * D * sizeof(float);
         if (n > most) most = n;
@@ -422,7 +441,7 @@ size_t layernorm_bwd_workspace(int rows, int D, int rpb) {
 
 size_t rmsnorm_bwd_workspace(int rows, int D) {
     if (rows < 1 || D < 8) return 0;
-    const NormPlan p = norm_plan(D / 8, rows, rows);
+    const NormPlan p = norm_plan(D / 8, 3, rows, rows);
     return 256 + static_cast<size_t>(p.parts) * D * sizeof(float);
 }
 
@@ -432,7 +451,7 @@ cudaError_t launch_layernorm_bwd(const void* dy, const float* x, const float* me
                                  unsigned long long* launches) {
     // without modulation all rows are one batch
     if (!scale || rpb > rows) rpb = rows;
-    const NormPlan p = norm_plan(D / 4, rows, rpb);
+    const NormPlan p = norm_plan(D / 4, 5, rows, rpb);
     const int kind = scale ? kGainScale : w ? kGainW : kGainOne;
     const void* gain = scale ? static_cast<const void*>(scale) : w;
     // one CTA a batch writes its sums in place, several write partial rows
@@ -470,7 +489,7 @@ cudaError_t launch_layernorm_bwd(const void* dy, const float* x, const float* me
 #undef DLO_LNB
     ++*launches;
     if (e != cudaSuccess || !sums || direct) return e != cudaSuccess ? e : cudaGetLastError();
-    e = launch_k(column_sums_kernel, sum_blocks(p.batches, 2, D / 4), 256, 0, s, ws, p.parts, D / 4, 2, dshift, dscale,
+    e = launch_k(column_sums_kernel, sum_blocks(p.batches, 2, D / 4), 1024, 0, s, ws, p.parts, D / 4, 2, dshift, dscale,
                  static_cast<size_t>(dmod_ld));
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -479,7 +498,7 @@ cudaError_t launch_layernorm_bwd(const void* dy, const float* x, const float* me
 cudaError_t launch_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx, const void* w, const float* rstd,
                                int rows, int D, void* dx, int lddx, float* dw, float* ws, cudaStream_t s,
                                unsigned long long* launches) {
-    const NormPlan p = norm_plan(D / 8, rows, rows);
+    const NormPlan p = norm_plan(D / 8, 3, rows, rows);
     float* sums = !dw ? nullptr : p.parts == 1 ? dw : ws;
     const int r = p.warps / p.w;
     const size_t smem = sums && r > 1 ? static_cast<size_t>(r) * D * sizeof(float) : 0;
@@ -491,26 +510,26 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx,
     const int v8 = (D / 8 + 32 * p.w - 1) / (32 * p.w);
 #define DLO_RMB(V, W, N) \
     e = launch_k(rmsnorm_bwd_kernel<V, W, N>, g, 32 * N, smem, s, d, lddy, xb, ldx, wb, rstd, rows, D, p.parts, o, lddx, sums)
+    // three 8-column pieces a thread: with the next row's in registers too, five
+    // would spill (8192 x 5120 rows: 89 us, 54 us with three)
     if (p.w == 1) {
         if (v8 <= 1) DLO_RMB(1, 1, 8);
-        else if (v8 <= 3) DLO_RMB(3, 1, 8);
-        else DLO_RMB(5, 1, 8);
+        else DLO_RMB(3, 1, 8);
     } else if (p.w == 2) {
-        if (v8 <= 3) DLO_RMB(3, 2, 8);
-        else DLO_RMB(5, 2, 8);
+        DLO_RMB(3, 2, 8);
     } else if (p.w == 4) {
-        if (v8 <= 3) DLO_RMB(3, 4, 8);
-        else DLO_RMB(5, 4, 8);
+        DLO_RMB(3, 4, 8);
     } else if (p.w == 8) {
-        if (v8 <= 3) DLO_RMB(3, 8, 8);
-        else DLO_RMB(5, 8, 8);
+        DLO_RMB(3, 8, 8);
+    } else if (p.w == 16) {
+        DLO_RMB(3, 16, 16);
     } else {
-        DLO_RMB(5, 16, 16);
+        DLO_RMB(3, 32, 32);
     }
 #undef DLO_RMB
     ++*launches;
     if (e != cudaSuccess || !sums || sums == dw) return e != cudaSuccess ? e : cudaGetLastError();
-    e = launch_k(column_sums_kernel, sum_blocks(1, 1, D / 4), 256, 0, s, ws, p.parts, D / 4, 1, dw, dw, static_cast<size_t>(0));
+    e = launch_k(column_sums_kernel, sum_blocks(1, 1, D / 4), 1024, 0, s, ws, p.parts, D / 4, 1, dw, dw, static_cast<size_t>(0));
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
