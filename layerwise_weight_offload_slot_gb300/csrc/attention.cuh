@@ -30,21 +30,27 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* main,
 }
 
 // [batch, rows, heads, hd] view of a bf16 matrix whose batch b, row r, head h
-// starts at base + (b * rows + r) * ld + h * hd; box of box_cols x 1 head x
-// 128 rows, columns past hd zero-filled.
+// starts at base + (b * rows + r) * ld + h * hd; box of box_cols x box_heads
+// heads x 128 / box_heads rows, columns past hd zero-filled.
 inline bool make_map4(CUtensorMap* m, const void* base, int batch, int rows, int heads, int hd, int ld,
-               int box_cols, CUtensorMapSwizzle sw) {
+                      int box_cols, CUtensorMapSwizzle sw, int box_heads = 1) {
     EncodeTiledFn enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(heads),
                           static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
     cuuint64_t strides[3] = {static_cast<cuuint64_t>(hd) * 2, static_cast<cuuint64_t>(ld) * 2,
                              static_cast<cuuint64_t>(ld) * 2 * static_cast<cuuint64_t>(rows)};
-    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), 1, 128, 1};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_heads),
+                         static_cast<cuuint32_t>(128 / box_heads), 1};
     cuuint32_t es[4] = {1, 1, 1, 1};
     return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
                es, CU_TENSOR_MAP_INTERLEAVE_NONE, sw, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// mbar_wait by a whole warp: the same answer in every lane.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
 
 // Dynamic shared memory of a kernel, set once per device (*done: a bit each).

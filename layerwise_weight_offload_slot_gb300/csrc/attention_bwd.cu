@@ -60,6 +60,10 @@ struct BwdArgs {
     uint4* stats;                 // [batch * heads][query tiles] operands of kStatBytes
     __nv_bfloat16 *dQ, *dK, *dV;
     int ldo, lddo, lddq, lddk, lddv;
+    // CTAs that share one gradient tile, each a part of its products' other
+    // axis, and the fp32 parts [splits][rows][heads * hd] that they leave
+    int splits_q, splits_k;
+    float *part_q, *part_k, *part_v;
     int* err;
 };
 
@@ -157,11 +161,6 @@ __device__ __forceinline__ void bwd_init(const BwdBars& m) {
     fence_mbar_init();
 }
 
-// mbar_wait by a whole warp: the same answer in every lane.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
-}
-
 // Loads in flight, for the drain: slots and the parity of each.
 struct InFlight {
     uint32_t on = 0, par = 0;
@@ -213,9 +212,9 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi_mid, uint32_t& lo) 
 }
 
 // One thread's part of an accumulator row (32-column chunks first, first +
-// step, ...) times `scale`, as bf16.
+// step, ...) times `scale`: to `part` in fp32 if that is set, else to `out` in bf16.
 template <int HDP>
-__device__ __forceinline__ void store_row(uint32_t t, __nv_bfloat16* out, int hd, bool live, float scale, int first,
+__device__ __forceinline__ void store_row(uint32_t t, __nv_bfloat16* out, float* part, int hd, bool live, float scale, int first,
                                           int step) {
 #pragma unroll 1
     for (int c = first; c < (HDP + 31) / 32; c += step) {
@@ -223,6 +222,15 @@ __device__ __forceinline__ void store_row(uint32_t t, __nv_bfloat16* out, int hd
         tmem_ld_32x32b_x32(t + c * 32, r);
         tmem_wait_ld_r(r);
         if (!live) continue;
+        if (part) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c * 32 + 4 * k < hd)
+                    *reinterpret_cast<float4*>(part + c * 32 + 4 * k) =
+                        make_float4(__uint_as_float(r[4 * k]) * scale, __uint_as_float(r[4 * k + 1]) * scale,
+                                    __uint_as_float(r[4 * k + 2]) * scale, __uint_as_float(r[4 * k + 3]) * scale);
+            continue;
+        }
 #pragma unroll
         for (int k4 = 0; k4 < 4; ++k4) {
             if (c * 32 + 8 * k4 < hd) {
@@ -241,6 +249,12 @@ __device__ __forceinline__ void zero_out(__nv_bfloat16* out, int ld, int n, int 
     const int c8 = hd / 8;
     for (int i = threadIdx.x; i < n * c8; i += kThreadsB)
         reinterpret_cast<uint4*>(out + static_cast<size_t>(i / c8) * ld)[i % c8] = make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void zero_out(float* out, int ld, int n, int hd) {
+    const int c4 = hd / 4;
+    for (int i = threadIdx.x; i < n * c4; i += kThreadsB)
+        reinterpret_cast<float4*>(out + static_cast<size_t>(i / c4) * ld)[i % c4] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
@@ -291,18 +305,25 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     // with a causal mask the last query tiles see the most keys: first
-    const int qt = gridDim.x - 1 - blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int qtiles = gridDim.x / g.splits_q, split = blockIdx.x % g.splits_q;
+    const int qt = qtiles - 1 - blockIdx.x / g.splits_q, h = blockIdx.y, b = blockIdx.z;
     const int row0 = qt * kTile, off = g.nk - g.nq;
 
     pdl_wait();
     const int qlen = seq_len(g.q_lens, b, g.nq), klen = seq_len(g.k_lens, b, g.nk);
     const int last = min(row0 + kTile, qlen) - 1;
-    const int n = last < row0 ? 0 : (key_end(last, off, g.causal_block, klen) + kTile - 1) / kTile;
-    uint4* stat = g.stats + ((static_cast<size_t>(b) * g.heads + h) * gridDim.x + qt) * (kStatBytes / 16);
+    const int all = last < row0 ? 0 : (key_end(last, off, g.causal_block, klen) + kTile - 1) / kTile;
+    // key tiles [j0, j0 + n) are this CTA's
+    const int per = (all + g.splits_q - 1) / g.splits_q, j0 = split * per, n = min(all, j0 + per) - j0;
+    uint4* stat = split ? nullptr : g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16);
     __nv_bfloat16* dq0 = g.dQ + (static_cast<size_t>(b) * g.nq + row0) * g.lddq + h * g.hd;
+    const int ldp = g.heads * g.hd;
+    float* part0 = g.splits_q == 1 ? nullptr
+                                   : g.part_q + ((static_cast<size_t>(split) * gridDim.z + b) * g.nq + row0) * ldp + h * g.hd;
     if (n <= 0) {
-        if (threadIdx.x < kTile) write_stat(stat, threadIdx.x, kNothing, 0.f);
-        zero_out(dq0, g.lddq, min(kTile, g.nq - row0), g.hd);
+        if (stat && threadIdx.x < kTile) write_stat(stat, threadIdx.x, kNothing, 0.f);
+        if (part0) zero_out(part0, ldp, min(kTile, g.nq - row0), g.hd);
+        else zero_out(dq0, g.lddq, min(kTile, g.nq - row0), g.hd);
         return;
     }
 
@@ -352,7 +373,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     };
     // keys behind k_lens end inside the last tile: its K rows there become zero
     // before the MMAs see it (its loads complete on raw0 instead)
-    const int fix = klen < g.nk && klen < n * kTile ? klen - (n - 1) * kTile : kTile;
+    const int fix = klen < g.nk && klen < (j0 + n) * kTile ? klen - (j0 + n - 1) * kTile : kTile;
 
     if (warp == 0) {
         // ---------------- TMA: K and V
@@ -369,7 +390,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 const bool raw = fix < kTile && j == n - 1;
                 const uint32_t full = raw ? m.raw0 : m.full + 8 * k.s;
                 mbar_arrive_expect_tx(full, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R_OFF + k.s * P::TILE, &maps.k, &maps.kt, hk, j * kTile, b, full);
+                load_tile<NB, TAIL>(sb + P::R_OFF + k.s * P::TILE, &maps.k, &maps.kt, hk, (j0 + j) * kTile, b, full);
                 if (!raw) in.add(k);
                 if (!mbar_wait(m.empty + 8 * v.s, v.ph ^ 1, abort_flag)) {
                     ok = false;
@@ -377,7 +398,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                     break;
                 }
                 mbar_arrive_expect_tx(m.full + 8 * v.s, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R_OFF + v.s * P::TILE, &maps.v, &maps.vt, hk, j * kTile, b, m.full + 8 * v.s);
+                load_tile<NB, TAIL>(sb + P::R_OFF + v.s * P::TILE, &maps.v, &maps.vt, hk, (j0 + j) * kTile, b, m.full + 8 * v.s);
                 in.add(v);
             }
         }
@@ -466,7 +487,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
         for (int c = 0; c < kGroups; ++c) delta += part[c * kTile + row];
         // -L in units of the raw score
-        if (e == 0) write_stat(stat, row, l2 == INFINITY ? kNothing : -l2 / g.scale_log2, -delta);
+        if (stat && e == 0) write_stat(stat, row, l2 == INFINITY ? kNothing : -l2 / g.scale_log2, -delta);
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint64_t scale2 = f32x2(g.scale_log2, g.scale_log2), neg_l2 = f32x2(-l2, -l2), neg_d = f32x2(-delta, -delta);
         bool ok = true;
@@ -495,7 +516,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             for (int c = 0; c < 32; c += 2)
                 f32x2_split(mul_f32x2(f32x2(p[c], p[c + 1]), add_f32x2(f32x2(__uint_as_float(r[c]), __uint_as_float(r[c + 1])), neg_d)),
                             p[c], p[c + 1]);
-            const int see = end - j * kTile - kCols * e;     // columns that this row sees
+            const int see = end - (j0 + j) * kTile - kCols * e;     // columns that this row sees
             if (see < kCols) {
 #pragma unroll
                 for (int c = 0; c < 32; ++c)
@@ -515,7 +536,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (lane == 0) fail();
         } else {
             tc_fence_after();
-            store_row<T::HDP>(tl + 384, dq0 + static_cast<size_t>(row) * g.lddq, g.hd, i < g.nq, g.scale, e, kGroups);
+            store_row<T::HDP>(tl + 384, dq0 + static_cast<size_t>(row) * g.lddq,
+                              part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < g.nq, g.scale, e, kGroups);
         }
     }
 
@@ -551,7 +573,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         return;
     }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int kt = blockIdx.x, hk = blockIdx.y, b = blockIdx.z;
+    const int kt = blockIdx.x / g.splits_k, split = blockIdx.x % g.splits_k, hk = blockIdx.y, b = blockIdx.z;
     const int key0 = kt * kTile, off = g.nk - g.nq;
     const int qtiles = (g.nq + kTile - 1) / kTile;
 
@@ -560,12 +582,22 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // query tiles [t0, t1) of each of the group's heads, one after the other
     const int t0 = max(0, query_begin(key0, off, g.causal_block)) / kTile;
     const int t1 = key0 < klen ? (qlen + kTile - 1) / kTile : 0;
-    const int per = max(0, t1 - t0), n = per * g.group;
+    const int per = max(0, t1 - t0), all = per * g.group;
+    // of these `all` steps, [i0, i0 + n) are this CTA's
+    const int share = (all + g.splits_k - 1) / g.splits_k, i0 = split * share, n = min(all, i0 + share) - i0;
     __nv_bfloat16* dk0 = g.dK + (static_cast<size_t>(b) * g.nk + key0) * g.lddk + hk * g.hd;
     __nv_bfloat16* dv0 = g.dV + (static_cast<size_t>(b) * g.nk + key0) * g.lddv + hk * g.hd;
-    if (n == 0) {
-        zero_out(dk0, g.lddk, min(kTile, g.nk - key0), g.hd);
-        zero_out(dv0, g.lddv, min(kTile, g.nk - key0), g.hd);
+    const int ldp = gridDim.y * g.hd;
+    const size_t part_at = ((static_cast<size_t>(split) * gridDim.z + b) * g.nk + key0) * ldp + hk * g.hd;
+    const bool parts = g.splits_k > 1;
+    if (n <= 0) {
+        if (parts) {
+            zero_out(g.part_k + part_at, ldp, min(kTile, g.nk - key0), g.hd);
+            zero_out(g.part_v + part_at, ldp, min(kTile, g.nk - key0), g.hd);
+        } else {
+            zero_out(dk0, g.lddk, min(kTile, g.nk - key0), g.hd);
+            zero_out(dv0, g.lddv, min(kTile, g.nk - key0), g.hd);
+        }
         return;
     }
 
@@ -614,7 +646,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, key0, b, m.a_full);
             load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.v, &maps.vt, hk, key0, b, m.a_full);
         }
-        int qt = t0, h = hk * g.group;
+        int qt = t0 + i0 % per, h = hk * g.group + i0 / per;
         for (int i = 0; i < n; ++i) {
             const Slot q = first(i), d = second(i);
             const bool raw = fix < kTile && qt == t1 - 1;
@@ -746,7 +778,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const uint32_t ts = tl + kCols * e;
         const uint64_t scale2 = f32x2(g.scale_log2, g.scale_log2);
         bool ok = true;
-        int qt = t0;
+        int qt = t0 + i0 % per;
         for (int i = 0; i < n; ++i) {
             const int lo = begin - (qt * kTile + kCols * e), hi = qlen - (qt * kTile + kCols * e);
             const bool cut = __any_sync(0xFFFFFFFFu, lo > 0 || hi < kCols);
@@ -829,7 +861,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             // even groups write dV, odd ones dK
             const bool k = e & 1;
             __nv_bfloat16* out = k ? dk0 + static_cast<size_t>(row) * g.lddk : dv0 + static_cast<size_t>(row) * g.lddv;
-            store_row<T::HDP>(tl + (k ? P::DK_COL : P::DV_COL), out, g.hd, key < g.nk, k ? g.scale : 1.f, e >> 1, kGroups / 2);
+            float* part = parts ? (k ? g.part_k : g.part_v) + part_at + static_cast<size_t>(row) * ldp : nullptr;
+            store_row<T::HDP>(tl + (k ? P::DK_COL : P::DV_COL), out, part, g.hd, key < g.nk, k ? g.scale : 1.f, e >> 1, kGroups / 2);
         }
     }
 
@@ -842,6 +875,84 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
 }
 
+// Adds the parts of a split gradient in order and rounds once.  One thread
+// eight columns; bound by reading the parts.
+struct JoinOne {
+    const float* part;
+    __nv_bfloat16* out;
+    int splits, ld, c8;          // c8: pieces of 8 columns a row
+    long long rows;
+};
+struct JoinArgs {
+    JoinOne one[3];
+};
+
+__global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ JoinArgs a) {
+    pdl_wait();
+    pdl_launch_dependents();
+    long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) {
+        const JoinOne& j = a.one[t];
+        const long long n = j.rows * j.c8;
+        if (i >= n) {
+            i -= n;
+            continue;
+        }
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+        const float4* p = reinterpret_cast<const float4*>(j.part) + 2 * i;
+#pragma unroll 4
+        for (int k = 0; k < j.splits; ++k, p += 2 * n) {
+            const float4 u = p[0], v = p[1];
+            x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
+            y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
+        }
+        const long long row = i / j.c8;
+        reinterpret_cast<uint4*>(j.out + row * j.ld)[i - row * j.c8] =
+            make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+        return;
+    }
+}
+
+// Splits and workspace, from the sizes alone.
+//   dQ: query tiles that do not fill the SMs share their keys, four key tiles
+//     or more to a CTA.
+//   dK, dV: likewise over the group's query tiles; with a causal mask also
+//     where the longest CTA (all query tiles) has more than an SM's share of
+//     the whole (3 sequences of 2047 tokens, 16 heads over 4: @@ us unsplit, @@ in two).
+struct BwdSplit {
+    int q, k;
+    size_t part_q, part_k, part_v, total;      // byte offsets
+};
+
+BwdSplit bwd_split(const dlo_attn& a) {
+    const long long qt = (a.nq + kTile - 1) / kTile, kt = (a.nk + kTile - 1) / kTile, group = a.heads / a.kv_heads;
+    const long long nq = qt * a.heads * a.batch, nk = kt * a.kv_heads * a.batch, steps = qt * group;
+    const auto fill = [](long long ctas, long long work) {
+        long long s = kGb300Sms / ctas;
+        if (s > work / 4) s = work / 4;
+        return s < 1 ? 1ll : s > 64 ? 64ll : s;
+    };
+    BwdSplit b;
+    long long sq = fill(nq, kt), sk = fill(nk, steps);
+    if (a.causal_block > 0) {
+        // about half of all steps are done
+        const long long mean = nk * steps / 2 / kGb300Sms + 1;
+        long long s = (steps + mean - 1) / mean;
+        if (s > steps / 8) s = steps / 8;
+        if (s > sk) sk = s > 64 ? 64 : s;
+    }
+    b.q = static_cast<int>(sq);
+    b.k = static_cast<int>(sk);
+    const size_t rq = static_cast<size_t>(a.batch) * a.nq * a.heads * a.head_dim * sizeof(float);
+    const size_t rk = static_cast<size_t>(a.batch) * a.nk * a.kv_heads * a.head_dim * sizeof(float);
+    b.part_q = static_cast<size_t>(a.batch) * a.heads * qt * kStatBytes;
+    b.part_k = b.part_q + (b.q > 1 ? b.q * rq : 0);
+    b.part_v = b.part_k + (b.k > 1 ? b.k * rk : 0);
+    b.total = b.part_v + (b.k > 1 ? b.k * rk : 0);
+    return b;
+}
+
 template <int NB, bool TAIL>
 cudaError_t run_bwd(const BwdMaps& maps, const BwdArgs& g, int batch, int kv_heads, cudaStream_t s,
                     unsigned long long* launches) {
@@ -850,10 +961,10 @@ cudaError_t run_bwd(const BwdMaps& maps, const BwdArgs& g, int batch, int kv_hea
     static unsigned long long set[2] = {0, 0};
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dq_kernel<NB, TAIL>), PQ::BYTES, &set[0]); e != cudaSuccess) return e;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dkv_kernel<NB, TAIL>), PK::BYTES, &set[1]); e != cudaSuccess) return e;
-    cudaError_t e = launch_k(dq_kernel<NB, TAIL>, dim3((g.nq + kTile - 1) / kTile, g.heads, batch), kThreadsB, PQ::BYTES, s, maps, g);
+    cudaError_t e = launch_k(dq_kernel<NB, TAIL>, dim3((g.nq + kTile - 1) / kTile * g.splits_q, g.heads, batch), kThreadsB, PQ::BYTES, s, maps, g);
     ++*launches;
     if (e != cudaSuccess) return e;
-    e = launch_k(dkv_kernel<NB, TAIL>, dim3((g.nk + kTile - 1) / kTile, kv_heads, batch), kThreadsB, PK::BYTES, s, maps, g);
+    e = launch_k(dkv_kernel<NB, TAIL>, dim3((g.nk + kTile - 1) / kTile * g.splits_k, kv_heads, batch), kThreadsB, PK::BYTES, s, maps, g);
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
@@ -861,7 +972,7 @@ cudaError_t run_bwd(const BwdMaps& maps, const BwdArgs& g, int batch, int kv_hea
 }  // namespace
 
 size_t attention_bwd_workspace(const dlo_attn& a) {
-    return static_cast<size_t>(a.batch) * a.heads * ((a.nq + kTile - 1) / kTile) * kStatBytes;
+    return bwd_split(a).total;
 }
 
 cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K, const void* V, const void* O,
@@ -883,6 +994,13 @@ cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K
     g.dO = static_cast<const __nv_bfloat16*>(dO);
     g.lse = lse;
     g.stats = static_cast<uint4*>(ws);
+    const BwdSplit split = bwd_split(a);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    g.splits_q = split.q;
+    g.splits_k = split.k;
+    g.part_q = reinterpret_cast<float*>(base + split.part_q);
+    g.part_k = reinterpret_cast<float*>(base + split.part_k);
+    g.part_v = reinterpret_cast<float*>(base + split.part_v);
     g.dQ = static_cast<__nv_bfloat16*>(dQ);
     g.dK = static_cast<__nv_bfloat16*>(dK);
     g.dV = static_cast<__nv_bfloat16*>(dV);
@@ -904,9 +1022,19 @@ cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K
     if (!map(&m.q, &m.qt, Q, a.nq, a.heads, a.ldq) || !map(&m.k, &m.kt, K, a.nk, a.kv_heads, a.ldk) ||
         !map(&m.v, &m.vt, V, a.nk, a.kv_heads, a.ldv) || !map(&m.d, &m.dt, dO, a.nq, a.heads, a.lddo))
         return cudaErrorInvalidValue;
-    if (hd <= 64) return run_bwd<1, false>(m, g, a.batch, a.kv_heads, s, launches);
-    if (tail) return run_bwd<1, true>(m, g, a.batch, a.kv_heads, s, launches);
-    return run_bwd<2, false>(m, g, a.batch, a.kv_heads, s, launches);
+    cudaError_t e = hd <= 64 ? run_bwd<1, false>(m, g, a.batch, a.kv_heads, s, launches)
+                    : tail   ? run_bwd<1, true>(m, g, a.batch, a.kv_heads, s, launches)
+                             : run_bwd<2, false>(m, g, a.batch, a.kv_heads, s, launches);
+    if (e != cudaSuccess || (split.q == 1 && split.k == 1)) return e;
+    const long long rq = static_cast<long long>(a.batch) * a.nq, rk = static_cast<long long>(a.batch) * a.nk;
+    const int cq = a.heads * hd / 8, ck = a.kv_heads * hd / 8;
+    const JoinArgs j = {{{g.part_q, g.dQ, split.q, a.lddq, cq, split.q > 1 ? rq : 0},
+                         {g.part_k, g.dK, split.k, a.lddk, ck, split.k > 1 ? rk : 0},
+                         {g.part_v, g.dV, split.k, a.lddv, ck, split.k > 1 ? rk : 0}}};
+    const long long n = j.one[0].rows * cq + 2 * j.one[1].rows * ck;
+    e = launch_k(bwd_join_kernel, static_cast<unsigned>((n + 255) / 256), 256, 0, s, j);
+    ++*launches;
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace dlo

@@ -84,6 +84,7 @@ struct AttnTrain {
     float* lse;                 // [batch, heads, nq]
     const int *q_lens, *k_lens;
     int causal_block, group, splits;
+    int lg;                     // 2^lg query heads of a group share a tile: row r is head r % 2^lg of query r >> lg
     float *po, *pl;             // splits > 1: [splits][batch][heads][nq][hd] and [..][nq]
 };
 
@@ -112,21 +113,25 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + P::TMEM_SLOT_OFF);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + P::ABORT_OFF);
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int h = blockIdx.y, b = blockIdx.z;
-    int qt = blockIdx.x, ntiles = (nk + TK - 1) / TK;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int b = blockIdx.z;
+    int h = blockIdx.y, qt = blockIdx.x, ntiles = (nk + TK - 1) / TK;
     int t0 = 0, hk = h, qlen = nq, klen = nk, split = 0;   // TR: first key tile, key/value head, valid rows
+    int nh = gridDim.y, tq = TQ;                           // TR: query heads, queries per tile
     if constexpr (TR) {
         pdl_wait();             // the lengths may come from the predecessor
         const int off = nk - nq;
         split = qt % tr.splits;
         // with a causal mask the last query tiles have the most keys: first
         qt = gridDim.x / tr.splits - 1 - qt / tr.splits;
+        h <<= tr.lg;            // the first of the tile's heads
+        nh <<= tr.lg;
+        tq >>= tr.lg;
         hk = h / tr.group;
         qlen = seq_len(tr.q_lens, b, nq);
         klen = seq_len(tr.k_lens, b, nk);
-        const int last = min(qt * TQ + TQ, qlen) - 1;
-        ntiles = last < qt * TQ ? 0 : (key_end(last, off, tr.causal_block, klen) + TK - 1) / TK;
+        const int last = min(qt * tq + tq, qlen) - 1;
+        ntiles = last < qt * tq ? 0 : (key_end(last, off, tr.causal_block, klen) + TK - 1) / TK;
         if (tr.splits > 1) {
             const int per = (ntiles + tr.splits - 1) / tr.splits;
             t0 = split * per;
@@ -134,16 +139,17 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         }
         if (ntiles <= 0) {      // no key for any of the rows
             pdl_launch_dependents();
-            const size_t rows0 = (static_cast<size_t>(b) * gridDim.y + h) * nq;
-            if (tr.splits > 1) {
-                float* pl = tr.pl + static_cast<size_t>(split) * gridDim.z * gridDim.y * nq + rows0;
-                for (int i = qt * TQ + threadIdx.x; i < min(nq, qt * TQ + TQ); i += kThreadsA) pl[i] = -INFINITY;
-            } else {
+            float* lse = tr.splits > 1 ? tr.pl + static_cast<size_t>(split) * gridDim.z * nh * nq : tr.lse;
+            const int rows = min(nq - qt * tq, tq) << tr.lg;
+            for (int r = threadIdx.x; r < rows; r += kThreadsA)
+                lse[(static_cast<size_t>(b) * nh + h + (r & ((1 << tr.lg) - 1))) * nq + qt * tq + (r >> tr.lg)] = -INFINITY;
+            if (tr.splits == 1) {
                 const int c8 = hd / 8;
-                for (int i = threadIdx.x; i < min(nq - qt * TQ, TQ) * c8; i += kThreadsA)
-                    reinterpret_cast<uint4*>(O + (static_cast<size_t>(b) * nq + qt * TQ + i / c8) * ldo + h * hd)[i % c8] =
-                        make_uint4(0, 0, 0, 0);
-                for (int i = qt * TQ + threadIdx.x; i < min(nq, qt * TQ + TQ); i += kThreadsA) tr.lse[rows0 + i] = -INFINITY;
+                for (int i = threadIdx.x; i < rows * c8; i += kThreadsA) {
+                    const int r = i / c8;
+                    reinterpret_cast<uint4*>(O + (static_cast<size_t>(b) * nq + qt * tq + (r >> tr.lg)) * ldo +
+                                             (h + (r & ((1 << tr.lg) - 1))) * hd)[i % c8] = make_uint4(0, 0, 0, 0);
+                }
             }
             return;
         }
@@ -174,7 +180,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
     pdl_wait();                 // predecessor's outputs complete and visible
     pdl_launch_dependents();
 
@@ -193,7 +199,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         uint32_t par = 0;         // parity of that load's phase
         if (lane == 0) {
             mbar_arrive_expect_tx(q_full, P::TILE);
-            load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * TQ, b, q_full);
+            load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * tq, b, q_full);
             for (int j = 0; ok && j < ntiles; ++j) {
                 const int st = j % NS;
                 const uint32_t ph = (j / NS) & 1;
@@ -233,8 +239,9 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             for (int i = 0; i < NS; ++i)
                 if (issued & (1u << i)) mbar_wait(kv_full + 8 * i, (par >> i) & 1u, nullptr);
         }
-    } else if (warp == 1 && lane == 0) {
-        // ---------------- MMA issuer
+    } else if (warp == 1) {
+        // ---------------- MMA issuer: the warp waits, one lane issues
+        const bool one = elect_one();
         constexpr uint32_t idesc_s = idesc_bf16_f32(TQ, TK);
         constexpr uint32_t idesc_o = idesc_bf16_f32(TQ, NB * 64, true);
         constexpr uint32_t idesc_ot = idesc_bf16_f32(TQ, 16, true);
@@ -249,7 +256,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         const uint64_t qt_desc = sw32_desc(sb + P::Q_OFF + NB * P::BLK);
         const uint64_t kt_desc0 = sw32_desc(sb + P::K_OFF + NB * P::BLK);
         const uint64_t vt_desc0 = sw32_desc(sb + P::V_OFF + NB * P::BLK);
-        bool ok = mbar_wait(q_full, 0, abort_flag);
+        bool ok = warp_wait(q_full, 0, abort_flag);
         auto issue_s = [&](int j) -> bool {
             const int st = j % NS;                 // K stage
             const uint32_t ph = (j / NS) & 1;
@@ -258,37 +265,43 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             // finished with them before p_full(j-2), and PV_{j-2}, issued
             // earlier by this thread, reads P_{j-2} before this MMA writes
             // (MMAs of one thread execute in issue order)
-            if (!mbar_wait(kv_full + 8 * st, ph, abort_flag)) return false;
+            if (!warp_wait(kv_full + 8 * st, ph, abort_flag)) return false;
             tc_fence_after();
             const uint32_t d = tmem + sbuf * TK;
             const uint32_t so = (st * P::TILE) >> 4;
+            if (one) {
 #pragma unroll
-            for (int kk = 0; kk < NB * 4; ++kk) {
-                const uint32_t off = ((kk >> 2) * P::BLK + (kk & 3) * 32) >> 4;
-                tc_mma_f16(d, q_desc + off, k_desc0 + so + off, idesc_s, kk > 0);
+                for (int kk = 0; kk < NB * 4; ++kk) {
+                    const uint32_t off = ((kk >> 2) * P::BLK + (kk & 3) * 32) >> 4;
+                    tc_mma_f16(d, q_desc + off, k_desc0 + so + off, idesc_s, kk > 0);
+                }
+                if constexpr (TAIL) tc_mma_f16(d, qt_desc, kt_desc0 + so, idesc_s, 1u);
+                tc_commit(s_full + 8 * sbuf);
+                tc_commit(k_empty + 8 * st);
             }
-            if constexpr (TAIL) tc_mma_f16(d, qt_desc, kt_desc0 + so, idesc_s, 1u);
-            tc_commit(s_full + 8 * sbuf);
-            tc_commit(k_empty + 8 * st);
+            __syncwarp();
             return true;
         };
         auto issue_pv = [&](int j) -> bool {
             const int st = j % NS;                 // V stage: landed with K_j (waited in issue_s)
             const int sbuf = j % P::SBUF;          // P lives in S buffer sbuf
-            if (!mbar_wait(p_full, j & 1, abort_flag)) return false;
+            if (!warp_wait(p_full, j & 1, abort_flag)) return false;
             tc_fence_after();
             const uint32_t so = (st * P::TILE) >> 4;
+            if (one) {
 #pragma unroll
-            for (int kk = 0; kk < TK / 16; ++kk) {
-                const uint32_t a = tmem + sbuf * TK + kk * 8;    // P_j: 16 keys = 8 columns
-                const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
-                tc_mma_f16_ts(tmem + P::O_COL, a, v_desc0 + so + ((kk * 2048) >> 4), idesc_o, acc);
-                if constexpr (TAIL)
-                    tc_mma_f16_ts(tmem + P::O_COL + NB * 64, a, vt_desc0 + so + ((kk * 512) >> 4), idesc_ot,
-                                  acc);
+                for (int kk = 0; kk < TK / 16; ++kk) {
+                    const uint32_t a = tmem + sbuf * TK + kk * 8;    // P_j: 16 keys = 8 columns
+                    const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
+                    tc_mma_f16_ts(tmem + P::O_COL, a, v_desc0 + so + ((kk * 2048) >> 4), idesc_o, acc);
+                    if constexpr (TAIL)
+                        tc_mma_f16_ts(tmem + P::O_COL + NB * 64, a, vt_desc0 + so + ((kk * 512) >> 4), idesc_ot,
+                                      acc);
+                }
+                tc_commit(pv_done);
+                tc_commit(v_empty + 8 * st);
             }
-            tc_commit(pv_done);
-            tc_commit(v_empty + 8 * st);
+            __syncwarp();
             return true;
         };
         if (ok) ok = issue_s(0);
@@ -297,11 +310,14 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         // (MMAs of one thread execute in issue order)
         for (int j = 1; ok && j < ntiles; ++j) ok = DUO ? (issue_pv(j - 1) && issue_s(j)) : (issue_s(j) && issue_pv(j - 1));
         if (ok) ok = issue_pv(ntiles - 1);
-        if (!ok) fail();
-        if (*abort_flag) {
-            tc_commit(drain);
-            mbar_wait(drain, 0, nullptr);
+        if (one) {
+            if (!ok) fail();
+            if (*abort_flag) {
+                tc_commit(drain);
+                mbar_wait(drain, 0, nullptr);
+            }
         }
+        __syncwarp();
     } else if (warp >= 2) {
         // ---------------- softmax: thread = query row
         const int q = warp & 3;
@@ -311,7 +327,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         bool ok = true;
         int row_end = nk;         // one past the last key of this row
         if constexpr (TR) {
-            const int i = qt * TQ + row;
+            const int i = qt * tq + (row >> tr.lg);
             row_end = i < qlen ? key_end(i, nk - nq, tr.causal_block, klen) : 0;
         }
         for (int j = 0; j < ntiles; ++j) {
@@ -407,14 +423,15 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         } else {
             tc_fence_after();
             const float inv = TR && l == 0.f ? 0.f : 1.f / l;
-            const int grow = qt * TQ + row;
+            const int grow = qt * tq + (TR ? row >> tr.lg : row);
+            if constexpr (TR) h += row & ((1 << tr.lg) - 1);
             float* prow = nullptr;
             if constexpr (TR) {
                 // natural logarithm of the sum of exp(scores)
                 const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
-                const size_t r = (static_cast<size_t>(b) * gridDim.y + h) * nq + grow;
+                const size_t r = (static_cast<size_t>(b) * nh + h) * nq + grow;
                 if (tr.splits > 1) {
-                    const size_t p = static_cast<size_t>(split) * gridDim.z * gridDim.y * nq + r;
+                    const size_t p = static_cast<size_t>(split) * gridDim.z * nh * nq + r;
                     prow = tr.po + p * hd;
                     if (grow < nq) tr.pl[p] = lse;
                 } else if (grow < nq) {
@@ -462,7 +479,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
 template <int NB, bool TAIL, bool DUO, bool TR = false>
 cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int batch, int heads,
                    int hd, int nq, int nk, int ldq, int ldk, int ldv, int ldo, int* err,
-                   cudaStream_t s, unsigned long long* launches, const AttnTrain& tr = AttnTrain{nullptr, nullptr, nullptr, 0, 1, 1, nullptr, nullptr}) {
+                   cudaStream_t s, unsigned long long* launches, const AttnTrain& tr = AttnTrain{nullptr, nullptr, nullptr, 0, 1, 1, 0, nullptr, nullptr}) {
     using P = AttnPlan<NB, TAIL, DUO>;
     static_assert(P::BYTES <= 227 * 1024, "attention shared memory plan exceeds 227 KB");
     const void* kernel = reinterpret_cast<const void*>(&attn_tc_kernel<NB, TAIL, DUO, TR>);
@@ -470,12 +487,13 @@ cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int bat
     if (cudaError_t e = allow_smem(kernel, P::BYTES, &attr); e != cudaSuccess) return e;
     AttnMaps maps;
     const CUtensorMapSwizzle w128 = CU_TENSOR_MAP_SWIZZLE_128B, w32 = CU_TENSOR_MAP_SWIZZLE_32B;
-    if (!make_map4(&maps.q, Q, batch, nq, heads, hd, ldq, 64, w128) ||
+    const int qh = 1 << tr.lg;
+    if (!make_map4(&maps.q, Q, batch, nq, heads, hd, ldq, 64, w128, qh) ||
         !make_map4(&maps.k, K, batch, nk, heads / tr.group, hd, ldk, 64, w128) ||
         !make_map4(&maps.v, V, batch, nk, heads / tr.group, hd, ldv, 64, w128))
         return cudaErrorInvalidValue;
     if (TAIL) {
-        if (!make_map4(&maps.qt, Q, batch, nq, heads, hd, ldq, 16, w32) ||
+        if (!make_map4(&maps.qt, Q, batch, nq, heads, hd, ldq, 16, w32, qh) ||
             !make_map4(&maps.kt, K, batch, nk, heads / tr.group, hd, ldk, 16, w32) ||
             !make_map4(&maps.vt, V, batch, nk, heads / tr.group, hd, ldv, 16, w32))
             return cudaErrorInvalidValue;
@@ -485,7 +503,8 @@ cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int bat
         maps.vt = maps.v;
     }
     const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
-    dim3 grid((nq + TQ - 1) / TQ * tr.splits, heads, batch);
+    const int tq = TQ >> tr.lg;
+    dim3 grid((nq + tq - 1) / tq * tr.splits, heads >> tr.lg, batch);
     cudaError_t le_ = launch_k(attn_tc_kernel<NB, TAIL, DUO, TR>, grid, kThreadsA, P::BYTES, s, maps, static_cast<__nv_bfloat16*>(O), hd, nq, nk, ldo, scale_log2, err, tr);
     ++*launches;
     return le_ != cudaSuccess ? le_ : cudaGetLastError();
@@ -558,32 +577,50 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const float* __restrict_
     if (lane == 0) lse[r] = total == 0.f ? -INFINITY : m + logf(total);
 }
 
-// CTAs that share the keys of one query tile: as many as fill the SMs when the
-// query tiles alone do not, each with at least four key tiles.  Sizes only.
-int attn_fwd_splits(const dlo_attn& a) {
-    const long long ctas = static_cast<long long>((a.nq + TQ - 1) / TQ) * a.heads * a.batch;
-    const long long fill = kGb300Sms / ctas, tiles = (a.nk + TK - 1) / TK / 4;
-    const long long n = fill < tiles ? fill : tiles;
-    return static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+// The grid of a training forward, from the sizes alone.
+//  lg: query heads of a group that share a tile (a power of two that divides
+//    the group), where that makes fewer tiles: short sequences leave most of a
+//    tile of one head empty and read K and V once a head (2 x 16 heads over
+//    4, 37 queries, 8192 keys: @@ us against @@).
+//  splits: CTAs that share the keys of one tile, as many as fill the SMs when
+//    the tiles alone do not, each with at least four key tiles.
+struct FwdPlan {
+    int lg, splits;
+    long long ctas;
+};
+
+FwdPlan attn_fwd_plan(const dlo_attn& a) {
+    const auto tiles = [&](int lg) {
+        const long long tq = TQ >> lg;
+        return (a.nq + tq - 1) / tq * (a.heads >> lg) * a.batch;
+    };
+    FwdPlan p = {0, 1, 0};
+    for (int lg = 1; lg <= 7 && (a.heads / a.kv_heads) % (1 << lg) == 0; ++lg)
+        if (tiles(lg) < tiles(p.lg)) p.lg = lg;
+    const long long ctas = tiles(p.lg), fill = kGb300Sms / ctas, keys = (a.nk + TK - 1) / TK / 4;
+    const long long n = fill < keys ? fill : keys;
+    p.splits = static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
+    p.ctas = ctas * p.splits;
+    return p;
 }
 
 }  // namespace
 
 size_t attention_fwd_workspace(const dlo_attn& a) {
     const size_t rows = static_cast<size_t>(a.batch) * a.heads * a.nq;
-    const int n = attn_fwd_splits(a);
+    const int n = attn_fwd_plan(a).splits;
     return 256 + (n > 1 ? n * rows * (a.head_dim + 1) * sizeof(float) : 0);
 }
 
 cudaError_t launch_attention_fwd(const dlo_attn& a, const void* Q, const void* K, const void* V, void* O, float* lse,
                                  void* ws, int* err, cudaStream_t s, unsigned long long* launches) {
     const size_t rows = static_cast<size_t>(a.batch) * a.heads * a.nq;
+    const FwdPlan plan = attn_fwd_plan(a);
     AttnTrain tr = {lse, a.q_lens, a.k_lens, a.causal_block < a.nk ? a.causal_block : a.nk, a.heads / a.kv_heads,
-                    attn_fwd_splits(a), static_cast<float*>(ws), nullptr};
+                    plan.splits, plan.lg, static_cast<float*>(ws), nullptr};
     tr.pl = tr.po + tr.splits * rows * a.head_dim;
     const int hd = a.head_dim;
-    const long long ctas = static_cast<long long>((a.nq + TQ - 1) / TQ) * a.heads * a.batch * tr.splits;
-    const bool duo = ctas > kGb300Sms;      // as for launch_attention_tc
+    const bool duo = plan.ctas > kGb300Sms;      // as for launch_attention_tc
     cudaError_t e;
 #define DLO_AF(NB, TAIL, DUO)                                                                                         e = run_tc<NB, TAIL, DUO, true>(Q, K, V, O, a.batch, a.heads, hd, a.nq, a.nk, a.ldq, a.ldk, a.ldv, a.ldo, err,                                     s, launches, tr)
     if (hd <= 64) {

@@ -185,6 +185,12 @@ CASES = [
     (2, 2, 2, 64, 130, 130, 0, [200, -3], [1 << 30, 50]),     # lengths out of range are taken into it
     (1, 2, 1, 64, 5, 4100, 0, None, [4001]),          # few queries: the keys are split
     (2, 2, 2, 128, 17, 5000, 1, [17, 9], [5000, 300]),
+    (1, 2, 2, 64, 2500, 100, 0, None, None),          # few keys: their gradients are split over the queries
+    (2, 4, 2, 72, 1500, 1500, 1, [1500, 900], [1500, 900]),   # causal: likewise
+    (2, 8, 2, 128, 33, 1300, 0, [33, 7], [1300, 515]),        # heads of a group share query tiles
+    (1, 24, 2, 64, 10, 700, 1, None, None),           # groups of 12: four heads a tile
+    (2, 16, 1, 40, 1, 260, 0, [1, 0], None),
+    (1, 8, 1, 72, 100, 90, 30, None, [50]),
 ]
 
 
