@@ -113,10 +113,10 @@ struct BwdPlan {
     static constexpr uint32_t DS_COL = DS_APART ? P_COL + 64 : 128;
     static constexpr int A0_OFF = 0, A1_OFF = TILE;
     static constexpr int R_OFF = 2 * TILE;
-    // dq: partial sums of D; dkv: the two selecting operands, then the statistics
+    // dq: D of each row; dkv: the two selecting operands, then the statistics
     static constexpr int SEL_OFF = R_OFF + SLOTS * TILE;
     static constexpr int STAT_OFF = SEL_OFF + 2 * kStatBytes;
-    static constexpr int BAR_OFF = DQ ? SEL_OFF + kGroups * kTile * 4 : STAT_OFF + STATS * kStatBytes;
+    static constexpr int BAR_OFF = DQ ? SEL_OFF + kTile * 4 : STAT_OFF + STATS * kStatBytes;
     // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, s_read, d_read; full, empty [SLOTS]
     static constexpr int NBARS = 12 + 2 * SLOTS;
     static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
@@ -327,25 +327,32 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         return;
     }
 
-    // D = rowsum(dO O) of row (threadIdx.x % 128), each group a part of the
-    // columns, all loads at once: they overlap the set-up
-    float* part = reinterpret_cast<float*>(smem + P::SEL_OFF);
+    // D = rowsum(dO O): LP lanes read one row's 16-byte pieces side by side, eight
+    // rows a warp, all loads at once: they overlap the set-up.  (One row a lane
+    // touches 32 rows a load instruction: set-up took 14000 cycles with 40 x 128
+    // columns a row, against @@.)
+    constexpr int LP = NB == 1 && !TAIL ? 8 : 16, RP = 32 / LP;
+    float* row_d = reinterpret_cast<float*>(smem + P::SEL_OFF);
     float l2 = INFINITY;                // L in units of log2
     if (warp >= 4) {
-        const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane, i = row0 + row;
-        uint4 o[4], d[4];
-        float l = -INFINITY, t = 0.f;
-        if (i < qlen) l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
+        uint4 o[8 / RP], d[8 / RP];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int c = e + kGroups * u;
-            const bool in = i < qlen && c < g.hd / 8;
-            o[u] = in ? reinterpret_cast<const uint4*>(g.O + (static_cast<size_t>(b) * g.nq + i) * g.ldo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
-            d[u] = in ? reinterpret_cast<const uint4*>(g.dO + (static_cast<size_t>(b) * g.nq + i) * g.lddo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
+        for (int u = 0; u < 8 / RP; ++u) {
+            const int row = (warp - 4) * 8 + u * RP + lane / LP, c = lane % LP;
+            const bool in = row0 + row < qlen && c < g.hd / 8;
+            const size_t r = static_cast<size_t>(b) * g.nq + row0 + row;
+            o[u] = in ? reinterpret_cast<const uint4*>(g.O + r * g.ldo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
+            d[u] = in ? reinterpret_cast<const uint4*>(g.dO + r * g.lddo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
         }
+        const int i = row0 + (warp & 3) * 32 + lane;
+        const float l = i < qlen ? g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i] : -INFINITY;
 #pragma unroll
-        for (int u = 0; u < 4; ++u) t += dot8(o[u], d[u]);
-        part[e * kTile + row] = t;
+        for (int u = 0; u < 8 / RP; ++u) {
+            float t = dot8(o[u], d[u]);
+#pragma unroll
+            for (int x = LP / 2; x > 0; x >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
+            if (lane % LP == 0) row_d[(warp - 4) * 8 + u * RP + lane / LP] = t;
+        }
         if (l != -INFINITY) l2 = l * 1.4426950408889634f;
     }
     if (threadIdx.x == 0) {
@@ -483,9 +490,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;    // group, TMEM lane
         const int i = row0 + row;
         const int end = i < qlen ? key_end(i, off, g.causal_block, klen) : 0;
-        float delta = 0.f;
-#pragma unroll
-        for (int c = 0; c < kGroups; ++c) delta += part[c * kTile + row];
+        const float delta = row_d[row];
         // -L in units of the raw score
         if (stat && e == 0) write_stat(stat, row, l2 == INFINITY ? kNothing : -l2 / g.scale_log2, -delta);
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
