@@ -29,6 +29,29 @@ __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* main,
     if constexpr (TAIL) tma_load_4d(dst + NB * T::BLK, tail, NB * 64, h, row0, b, bar);
 }
 
+// Columns [32 c, 32 c + 32) of row `row` as bf16 (w: 16 pairs) into such a tile,
+// in the layout that TMA stores from and loads to.
+template <int NB, bool TAIL>
+__device__ __forceinline__ void put_row(uint8_t* tile, int row, int c, const uint32_t (&w)[16]) {
+    using T = AttnTile<NB, TAIL>;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint4 v = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+        if (c < 2 * NB)
+            *reinterpret_cast<uint4*>(tile + (c >> 1) * T::BLK + row * 128 + ((((c & 1) * 4 + k) ^ (row & 7)) << 4)) = v;
+        else if (TAIL && k < 2)
+            *reinterpret_cast<uint4*>(tile + NB * T::BLK + row * 32 + ((k ^ ((row >> 2) & 1)) << 4)) = v;
+    }
+}
+
+template <int NB, bool TAIL>
+__device__ __forceinline__ void store_tile(uint32_t src, const CUtensorMap* main, const CUtensorMap* tail, int h, int row0, int b) {
+    using T = AttnTile<NB, TAIL>;
+#pragma unroll
+    for (int blk = 0; blk < NB; ++blk) tma_store_4d(main, src + blk * T::BLK, blk * 64, h, row0, b);
+    if constexpr (TAIL) tma_store_4d(tail, src + NB * T::BLK, NB * 64, h, row0, b);
+}
+
 // [batch, rows, heads, hd] view of a bf16 matrix whose batch b, row r, head h
 // starts at base + (b * rows + r) * ld + h * hd; box of box_cols x box_heads
 // heads x 128 / box_heads rows, columns past hd zero-filled.

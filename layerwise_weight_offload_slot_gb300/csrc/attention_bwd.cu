@@ -49,6 +49,8 @@ constexpr int kStatBytes = kTile * 32;
 struct BwdMaps {
     CUtensorMap q, k, v, d;       // 64-column boxes, 128-byte swizzle (d: dO)
     CUtensorMap qt, kt, vt, dt;   // 16-column tails, 32-byte swizzle
+    CUtensorMap gq, gk, gv;       // the gradients, likewise
+    CUtensorMap gqt, gkt, gvt;
 };
 
 struct BwdArgs {
@@ -117,8 +119,8 @@ struct BwdPlan {
     static constexpr int SEL_OFF = R_OFF + SLOTS * TILE;
     static constexpr int STAT_OFF = SEL_OFF + 2 * kStatBytes;
     static constexpr int BAR_OFF = DQ ? SEL_OFF + kTile * 4 : STAT_OFF + STATS * kStatBytes;
-    // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, s_read, d_read; full, empty [SLOTS]
-    static constexpr int NBARS = 12 + 2 * SLOTS;
+    // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, s_read, d_read, staged; full, empty [SLOTS]
+    static constexpr int NBARS = 13 + 2 * SLOTS;
     static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
     static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
     static constexpr int USED = ABORT_OFF + 4;
@@ -131,13 +133,13 @@ struct BwdPlan {
 };
 
 struct BwdBars {
-    uint32_t a_full, raw0, raw1, s_full, d_full, e0, e1, done, drain, s_read, d_read, full, empty;
+    uint32_t a_full, raw0, raw1, s_full, d_full, e0, e1, done, drain, s_read, d_read, staged, full, empty;
 };
 
 template <int SLOTS>
 __device__ __forceinline__ BwdBars bwd_bars(uint32_t b) {
     return {b, b + 8, b + 16, b + 24, b + 40, b + 48, b + 56, b + 64, b + 72, b + 80, b + 88,
-            b + 96, b + 96 + 8 * SLOTS};
+            b + 96, b + 104, b + 104 + 8 * SLOTS};
 }
 
 template <int SLOTS>
@@ -152,6 +154,7 @@ __device__ __forceinline__ void bwd_init(const BwdBars& m) {
     mbar_init(m.e1, 4 * kGroups);
     mbar_init(m.s_read, 4 * kGroups);
     mbar_init(m.d_read, 4 * kGroups);
+    mbar_init(m.staged, 4 * kGroups);
     mbar_init(m.done, 1);
     mbar_init(m.drain, 1);
     for (int i = 0; i < SLOTS; ++i) {
@@ -212,34 +215,28 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi_mid, uint32_t& lo) 
 }
 
 // One thread's part of an accumulator row (32-column chunks first, first +
-// step, ...) times `scale`: to `part` in fp32 if that is set, else to `out` in bf16.
-template <int HDP>
-__device__ __forceinline__ void store_row(uint32_t t, __nv_bfloat16* out, float* part, int hd, bool live, float scale, int first,
+// step, ...) times `scale`: in fp32 to `part` if that is set, else in bf16 to the
+// tile in shared memory that TMA then stores (rows and columns past the tensor
+// are not written).
+template <int NB, bool TAIL>
+__device__ __forceinline__ void store_row(uint32_t t, uint8_t* tile, int row, float* part, int hd, bool live, float scale, int first,
                                           int step) {
 #pragma unroll 1
-    for (int c = first; c < (HDP + 31) / 32; c += step) {
-        uint32_t r[32];
+    for (int c = first; c < (AttnTile<NB, TAIL>::HDP + 31) / 32; c += step) {
+        uint32_t r[32], w[16];
         tmem_ld_32x32b_x32(t + c * 32, r);
         tmem_wait_ld_r(r);
-        if (!live) continue;
         if (part) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (c * 32 + 4 * k < hd)
+                if (live && c * 32 + 4 * k < hd)
                     *reinterpret_cast<float4*>(part + c * 32 + 4 * k) =
                         make_float4(__uint_as_float(r[4 * k]) * scale, __uint_as_float(r[4 * k + 1]) * scale,
                                     __uint_as_float(r[4 * k + 2]) * scale, __uint_as_float(r[4 * k + 3]) * scale);
-            continue;
-        }
+        } else {
 #pragma unroll
-        for (int k4 = 0; k4 < 4; ++k4) {
-            if (c * 32 + 8 * k4 < hd) {
-                uint32_t w[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u)
-                    w[u] = pack_bf16x2(__uint_as_float(r[8 * k4 + 2 * u]) * scale, __uint_as_float(r[8 * k4 + 2 * u + 1]) * scale);
-                *reinterpret_cast<uint4*>(out + c * 32 + 8 * k4) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
+            for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
+            put_row<NB, TAIL>(tile, row, c, w);
         }
     }
 }
@@ -333,9 +330,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // columns a row, against @@.)
     constexpr int LP = NB == 1 && !TAIL ? 8 : 16, RP = 32 / LP;
     float* row_d = reinterpret_cast<float*>(smem + P::SEL_OFF);
-    float l2 = INFINITY;                // L in units of log2
+    uint4 o[8 / RP], d[8 / RP];
+    float l = -INFINITY;
     if (warp >= 4) {
-        uint4 o[8 / RP], d[8 / RP];
 #pragma unroll
         for (int u = 0; u < 8 / RP; ++u) {
             const int row = (warp - 4) * 8 + u * RP + lane / LP, c = lane % LP;
@@ -345,19 +342,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             d[u] = in ? reinterpret_cast<const uint4*>(g.dO + r * g.lddo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
         }
         const int i = row0 + (warp & 3) * 32 + lane;
-        const float l = i < qlen ? g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i] : -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 8 / RP; ++u) {
-            float t = dot8(o[u], d[u]);
-#pragma unroll
-            for (int x = LP / 2; x > 0; x >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
-            if (lane % LP == 0) row_d[(warp - 4) * 8 + u * RP + lane / LP] = t;
-        }
-        if (l != -INFINITY) l2 = l * 1.4426950408889634f;
+        if (i < qlen) l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
     }
     if (threadIdx.x == 0) {
         bwd_init<P::SLOTS>(m);
         *abort_flag = 0;
+        // this thread is also the one that loads: the first tiles need not wait
+        // for the rest of the set-up
+        mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
+        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, row0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, row0, b, m.a_full);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -388,9 +382,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         InFlight in;
         if (lane == 0) {
             const int hk = h / g.group;
-            mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
-            load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, row0, b, m.a_full);
-            load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, row0, b, m.a_full);
             for (int j = 0; j < n; ++j) {
                 const Slot k = first(j), v = second(j);
                 if (!mbar_wait(m.empty + 8 * k.s, k.ph ^ 1, abort_flag)) { ok = false; break; }
@@ -490,7 +481,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;    // group, TMEM lane
         const int i = row0 + row;
         const int end = i < qlen ? key_end(i, off, g.causal_block, klen) : 0;
-        const float delta = row_d[row];
+#pragma unroll
+        for (int u = 0; u < 8 / RP; ++u) {
+            float t = dot8(o[u], d[u]);
+#pragma unroll
+            for (int x = LP / 2; x > 0; x >>= 1) t += __shfl_xor_sync(0xFFFFFFFFu, t, x);
+            if (lane % LP == 0) row_d[(warp - 4) * 8 + u * RP + lane / LP] = t;
+        }
+        // every elementwise warp gets here: no wait comes before
+        asm volatile("bar.sync 1, %0;" ::"n"(kThreadsB - 128) : "memory");
+        const float delta = row_d[row], l2 = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;   // L in units of log2
         // -L in units of the raw score
         if (stat && e == 0) write_stat(stat, row, l2 == INFINITY ? kNothing : -l2 / g.scale_log2, -delta);
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
@@ -541,8 +541,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (lane == 0) fail();
         } else {
             tc_fence_after();
-            store_row<T::HDP>(tl + 384, dq0 + static_cast<size_t>(row) * g.lddq,
-                              part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < g.nq, g.scale, e, kGroups);
+            // the slots' tiles have all been read: the first one takes the result
+            store_row<NB, TAIL>(tl + 384, smem + P::R_OFF, row, part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < g.nq,
+                                g.scale, e, kGroups);
+            if (!part0) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m.staged);
+                if (warp == 4) {
+                    ok = warp_wait(m.staged, 0, abort_flag);
+                    if (lane == 0) {
+                        if (ok) {
+                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gq, &maps.gqt, h, row0, b);
+                            bulk_commit();
+                            bulk_wait_all();
+                        } else {
+                            fail();
+                        }
+                    }
+                }
+            }
         }
     }
 
@@ -609,6 +627,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     if (threadIdx.x == 0) {
         bwd_init<P::SLOTS>(m);
         *abort_flag = 0;
+        mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
+        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, key0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.v, &maps.vt, hk, key0, b, m.a_full);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -646,11 +667,6 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         bool ok = true;
         InFlight in;
         uint32_t raws = 0;        // tiles fixed so far
-        if (lane == 0) {
-            mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
-            load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, key0, b, m.a_full);
-            load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.v, &maps.vt, hk, key0, b, m.a_full);
-        }
         int qt = t0 + i0 % per, h = hk * g.group + i0 / per;
         for (int i = 0; i < n; ++i) {
             const Slot q = first(i), d = second(i);
@@ -863,11 +879,29 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (lane == 0) fail();
         } else {
             tc_fence_after();
-            // even groups write dV, odd ones dK
+            // even groups bring dV, odd ones dK, into the first two slots
             const bool k = e & 1;
-            __nv_bfloat16* out = k ? dk0 + static_cast<size_t>(row) * g.lddk : dv0 + static_cast<size_t>(row) * g.lddv;
             float* part = parts ? (k ? g.part_k : g.part_v) + part_at + static_cast<size_t>(row) * ldp : nullptr;
-            store_row<T::HDP>(tl + (k ? P::DK_COL : P::DV_COL), out, part, g.hd, key < g.nk, k ? g.scale : 1.f, e >> 1, kGroups / 2);
+            store_row<NB, TAIL>(tl + (k ? P::DK_COL : P::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < g.nk,
+                                k ? g.scale : 1.f, e >> 1, kGroups / 2);
+            if (!parts) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(m.staged);
+                if (warp == 4) {
+                    ok = warp_wait(m.staged, 0, abort_flag);
+                    if (lane == 0) {
+                        if (ok) {
+                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gv, &maps.gvt, hk, key0, b);
+                            store_tile<NB, TAIL>(sb + P::R_OFF + P::TILE, &maps.gk, &maps.gkt, hk, key0, b);
+                            bulk_commit();
+                            bulk_wait_all();
+                        } else {
+                            fail();
+                        }
+                    }
+                }
+            }
         }
     }
 
@@ -1025,7 +1059,9 @@ cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K
         return true;
     };
     if (!map(&m.q, &m.qt, Q, a.nq, a.heads, a.ldq) || !map(&m.k, &m.kt, K, a.nk, a.kv_heads, a.ldk) ||
-        !map(&m.v, &m.vt, V, a.nk, a.kv_heads, a.ldv) || !map(&m.d, &m.dt, dO, a.nq, a.heads, a.lddo))
+        !map(&m.v, &m.vt, V, a.nk, a.kv_heads, a.ldv) || !map(&m.d, &m.dt, dO, a.nq, a.heads, a.lddo) ||
+        !map(&m.gq, &m.gqt, dQ, a.nq, a.heads, a.lddq) || !map(&m.gk, &m.gkt, dK, a.nk, a.kv_heads, a.lddk) ||
+        !map(&m.gv, &m.gvt, dV, a.nk, a.kv_heads, a.lddv))
         return cudaErrorInvalidValue;
     cudaError_t e = hd <= 64 ? run_bwd<1, false>(m, g, a.batch, a.kv_heads, s, launches)
                     : tail   ? run_bwd<1, true>(m, g, a.batch, a.kv_heads, s, launches)
