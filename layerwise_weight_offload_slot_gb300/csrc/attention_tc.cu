@@ -91,6 +91,7 @@ struct AttnTrain {
 struct AttnMaps {
     CUtensorMap q, k, v;        // 64-column boxes, 128-byte swizzle
     CUtensorMap qt, kt, vt;     // 16-column tail boxes, 32-byte swizzle
+    CUtensorMap o, ot;          // TR: the output, stored by TMA
 };
 
 template <int NB, bool TAIL, bool DUO, bool TR>
@@ -106,7 +107,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     const uint32_t bar = sb + P::BAR_OFF;
     const uint32_t q_full = bar;
     const uint32_t kv_full = bar + 8, k_empty = bar + 32;
-    const uint32_t raw = bar + 56, v_empty = bar + 80;
+    const uint32_t raw = bar + 56, staged = bar + 64, v_empty = bar + 80;
     const uint32_t s_full = bar + 104;
     const uint32_t p_full = bar + 120, pv_done = bar + 128, drain = bar + 136;
     constexpr int NS = P::STAGES;
@@ -166,9 +167,16 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         mbar_init(p_full, 4);
         mbar_init(pv_done, 1);
         mbar_init(drain, 1);
-        if constexpr (TR) mbar_init(raw, 1);
+        if constexpr (TR) {
+            mbar_init(raw, 1);
+            mbar_init(staged, 4);
+        }
         *abort_flag = 0;
         fence_mbar_init();
+        if constexpr (TR) {     // this thread is the one that loads, and has waited for the predecessor
+            mbar_arrive_expect_tx(q_full, P::TILE);
+            load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * tq, b, q_full);
+        }
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -198,8 +206,10 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         uint32_t issued = 0;      // stages with a load in flight
         uint32_t par = 0;         // parity of that load's phase
         if (lane == 0) {
-            mbar_arrive_expect_tx(q_full, P::TILE);
-            load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * tq, b, q_full);
+            if constexpr (!TR) {
+                mbar_arrive_expect_tx(q_full, P::TILE);
+                load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * tq, b, q_full);
+            }
             for (int j = 0; ok && j < ntiles; ++j) {
                 const int st = j % NS;
                 const uint32_t ph = (j / NS) & 1;
@@ -424,6 +434,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             tc_fence_after();
             const float inv = TR && l == 0.f ? 0.f : 1.f / l;
             const int grow = qt * tq + (TR ? row >> tr.lg : row);
+            const int h0 = h;
             if constexpr (TR) h += row & ((1 << tr.lg) - 1);
             float* prow = nullptr;
             if constexpr (TR) {
@@ -444,10 +455,20 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(tl + P::O_COL + c * 32, r);
                 tmem_wait_ld_r(r);
+                if constexpr (TR) {
+                    if (!prow) {        // into Q's place, which every product has read
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            w[i] = pack_bf16x2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
+                        put_row<NB, TAIL>(smem + P::Q_OFF, row, c, w);
+                        continue;
+                    }
+                }
                 if (grow < nq) {
 #pragma unroll
                     for (int k4 = 0; k4 < 4; ++k4) {
-                        if (TR && prow && c * 32 + 8 * k4 < hd) {
+                        if (TR && c * 32 + 8 * k4 < hd) {
                             float4* pw = reinterpret_cast<float4*>(prow + c * 32 + 8 * k4);
 #pragma unroll
                             for (int u = 0; u < 2; ++u)
@@ -461,6 +482,22 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
                             w.w = pack_bf16x2(__uint_as_float(r[8 * k4 + 6]) * inv, __uint_as_float(r[8 * k4 + 7]) * inv);
                             *reinterpret_cast<uint4*>(orow + c * 32 + 8 * k4) = w;
                         }
+                    }
+                }
+            }
+            if constexpr (TR) {
+                if (!prow) {
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(staged);
+                    if (warp == 2 && warp_wait(staged, 0, abort_flag)) {
+                        if (lane == 0) {
+                            store_tile<NB, TAIL>(sb + P::Q_OFF, &maps.o, &maps.ot, h0, qt * tq, b);
+                            bulk_commit();
+                            bulk_wait_all();
+                        }
+                    } else if (warp == 2 && lane == 0) {
+                        fail();
                     }
                 }
             }
@@ -501,6 +538,13 @@ cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int bat
         maps.qt = maps.q;
         maps.kt = maps.k;
         maps.vt = maps.v;
+    }
+    maps.o = maps.q;
+    maps.ot = maps.qt;
+    if (TR) {
+        if (!make_map4(&maps.o, O, batch, nq, heads, hd, ldo, 64, w128, qh) ||
+            (TAIL && !make_map4(&maps.ot, O, batch, nq, heads, hd, ldo, 16, w32, qh)))
+            return cudaErrorInvalidValue;
     }
     const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
     const int tq = TQ >> tr.lg;
