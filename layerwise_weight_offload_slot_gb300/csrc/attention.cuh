@@ -76,17 +76,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
 
-// Dynamic shared memory of a kernel, set once per device (*done: a bit each).
-inline cudaError_t allow_smem(const void* kernel, int bytes, unsigned long long* done) {
-    int dev = 0;
-    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
-    const unsigned long long bit = 1ull << (dev & 63);
-    if (__atomic_load_n(done, __ATOMIC_ACQUIRE) & bit) return cudaSuccess;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELEASE);
-    return e;
-}
-
 // Rows [from, 128) of a tile set to zero by `step` threads, this one the lane-th.  Rows behind a sequence's
 // end may hold anything; as the contracted index of a product they would turn
 // a zero probability times an infinity into NaN.  The caller's mbarrier arrival

@@ -599,16 +599,23 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const float* __restrict_
     const int lane = threadIdx.x & 31;
     const size_t r = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;     // (b, h, i)
     if (r >= rows) return;
-    float top = -INFINITY;
-    for (int p = 0; p < splits; ++p) top = fmaxf(top, pl[p * rows + r]);
+    // lane p holds the weights of parts p and p + 32 (splits <= 64)
+    const float l0 = lane < splits ? pl[lane * rows + r] : -INFINITY;
+    const float l1 = lane + 32 < splits ? pl[(lane + 32) * rows + r] : -INFINITY;
+    float top = fmaxf(l0, l1);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
     const float m = top == -INFINITY ? 0.f : top;
-    float total = 0.f;
+    const float w0 = exp2f((l0 - m) * 1.4426950408889634f), w1 = exp2f((l1 - m) * 1.4426950408889634f);
+    float total = w0 + w1;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);      // columns 4 lane .. 4 lane + 3
+#pragma unroll 4
     for (int p = 0; p < splits; ++p) {
-        const float w = exp2f((pl[p * rows + r] - m) * 1.4426950408889634f);
-        if (w == 0.f) continue;                        // nothing visible there: its O_p was not written
-        total += w;
-        if (4 * lane < hd) {
+        const float w = __shfl_sync(0xFFFFFFFFu, p < 32 ? w0 : w1, p & 31);
+        // weight 0: nothing visible there, its O_p was not written
+        if (4 * lane < hd && w != 0.f) {
             const float4 v = reinterpret_cast<const float4*>(po + (p * rows + r) * hd)[lane];
             acc = make_float4(acc.x + w * v.x, acc.y + w * v.y, acc.z + w * v.z, acc.w + w * v.w);
         }

@@ -32,6 +32,27 @@ cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// Dynamic shared memory of a kernel, set once per device (*done: a bit each).
+inline cudaError_t allow_smem(const void* kernel, int bytes, unsigned long long* done) {
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev); e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (__atomic_load_n(done, __ATOMIC_ACQUIRE) & bit) return cudaSuccess;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) __atomic_fetch_or(done, bit, __ATOMIC_RELEASE);
+    return e;
+}
+
+// launch_k of a kernel that may take more than 48 KB of dynamic shared memory (up
+// to 200 KB beside its static variables).
+template <auto Kernel, typename... Args>
+cudaError_t launch_big(dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args&&... args) {
+    static unsigned long long set = 0;
+    if (smem > 48 * 1024)
+        if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(Kernel), 200 * 1024, &set); e != cudaSuccess) return e;
+    return launch_k(Kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
+}
+
 // ------------------------------------------------------------------ layout
 
 // Linear weights stored as E4M3 codes (W8A16 or W8A8).

@@ -62,6 +62,21 @@ __device__ __forceinline__ void row_totals(float& v0, float& v1, float (*red)[2]
     }
 }
 
+// 16 (or 8) bytes from global to this thread's own place in shared memory, zeros
+// where `in` is false; no barrier is needed between a thread's copies and its
+// reads of them, only its own wait.
+__device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(void* dst, const void* src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // What multiplies dy before the row sums: nothing, w (bf16) or 1 + scale (fp32)
 enum { kGainOne = 0, kGainW = 1, kGainScale = 2 };
 
@@ -190,6 +205,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
     }
 }
 
+// Places of the ring: one row in use, whose place is filled again only in the
+// next step, when every value read from it has been used, the others in flight.
+__host__ __device__ constexpr int ring_rows(int warps) { return warps == 32 ? 2 : 4; }
+
 // RMSNorm backward on bf16 rows of strides ldy, ldx, lddx: dx may be dy or x
 // (each element is read by the thread that writes it, before it writes).
 template <int V8, int W, int WARPS>
@@ -198,7 +217,7 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
                        const __nv_bfloat16* __restrict__ w, const float* __restrict__ rstd, int rows, int D, int parts,
                        __nv_bfloat16* dx, int lddx, float* __restrict__ sums) {
     constexpr int R = WARPS / W;
-    extern __shared__ float4 sh[];                  // [R][D / 4] when R > 1
+    extern __shared__ float4 sh[];                  // the ring; at the end [R][D / 4] when R > 1
     __shared__ float red[2][2][WARPS];
     pdl_wait();
     pdl_launch_dependents();
@@ -215,10 +234,9 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
 #pragma unroll
         for (int k = 0; k < 8; ++k) s[j][k] = 0.f;
     }
-    // the next row's pieces are on their way while this one's are used
-    uint4 xn[V8], dn[V8];
-    float rn = 0.f;
-    const auto load = [&](int r) {
+    constexpr int T = 32 * WARPS, N = ring_rows(WARPS);
+    uint4* ring = reinterpret_cast<uint4*>(sh) + threadIdx.x;          // [N][2 V8][T]
+    const auto load = [&](int r, int stage) {
         const bool live = r + rg < rows;
         const size_t row = live ? r + rg : 0;
         const uint4* xr = reinterpret_cast<const uint4*>(x + row * ldx);
@@ -227,24 +245,28 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
         for (int j = 0; j < V8; ++j) {
             const int i = t0 + 32 * W * j;
             const bool in = live && i < n8;
-            xn[j] = in ? xr[i] : make_uint4(0, 0, 0, 0);
-            dn[j] = in ? dyr[i] : make_uint4(0, 0, 0, 0);
+            copy16(ring + (stage * 2 * V8 + j) * T, xr + (in ? i : 0), in);
+            copy16(ring + (stage * 2 * V8 + V8 + j) * T, dyr + (in ? i : 0), in);
         }
-        rn = live ? rstd[row] : 0.f;
+        copies_commit();
     };
-    load(blockIdx.x * R);
-    int turn = 0;
-    for (int r = blockIdx.x * R; r < rows; r += parts * R, turn ^= 1) {
+    const int step = parts * R;
+#pragma unroll
+    for (int k = 0; k < N - 1; ++k) load(blockIdx.x * R + k * step, k);
+    int turn = 0, stage = 0;
+    for (int r = blockIdx.x * R; r < rows; r += step, turn ^= 1) {
         const bool live = r + rg < rows;
         const size_t row = live ? r + rg : r;
+        copies_wait<N - 2>();
         uint4 xv[V8], dv[V8];
 #pragma unroll
         for (int j = 0; j < V8; ++j) {
-            xv[j] = xn[j];
-            dv[j] = dn[j];
+            xv[j] = ring[(stage * 2 * V8 + j) * T];
+            dv[j] = ring[(stage * 2 * V8 + V8 + j) * T];
         }
-        const float rs = rn;
-        load(r + parts * R);
+        load(r + (N - 1) * step, (stage + N - 1) % N);
+        stage = (stage + 1) % N;
+        const float rs = rstd[row];
         float c = 0.f, unused = 0.f;
 #pragma unroll
         for (int j = 0; j < V8; ++j) {
@@ -283,6 +305,10 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
     }
     if (!sums) return;
     float4* o = reinterpret_cast<float4*>(sums + static_cast<size_t>(blockIdx.x) * D);
+    if constexpr (R > 1) {
+        copies_wait<0>();           // the ring's place is used again
+        __syncthreads();
+    }
     float4* mine = R == 1 ? o : sh + rg * 2 * n8;
 #pragma unroll
     for (int j = 0; j < V8; ++j) {
@@ -501,15 +527,17 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx,
     const NormPlan p = norm_plan(D / 8, 3, rows, rows);
     float* sums = !dw ? nullptr : p.parts == 1 ? dw : ws;
     const int r = p.warps / p.w;
-    const size_t smem = sums && r > 1 ? static_cast<size_t>(r) * D * sizeof(float) : 0;
+    const int v8 = (D / 8 + 32 * p.w - 1) / (32 * p.w), pieces = v8 <= 1 && p.w == 1 ? 1 : 3;
+    const size_t ring = static_cast<size_t>(ring_rows(p.warps)) * 2 * pieces * 32 * p.warps * sizeof(uint4);
+    const size_t end = sums && r > 1 ? static_cast<size_t>(r) * D * sizeof(float) : 0;
+    const size_t smem = ring > end ? ring : end;
     const unsigned g = static_cast<unsigned>(p.parts);
     const __nv_bfloat16 *d = static_cast<const __nv_bfloat16*>(dy), *xb = static_cast<const __nv_bfloat16*>(x),
                         *wb = static_cast<const __nv_bfloat16*>(w);
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dx);
     cudaError_t e = cudaErrorInvalidValue;
-    const int v8 = (D / 8 + 32 * p.w - 1) / (32 * p.w);
 #define DLO_RMB(V, W, N) \
-    e = launch_k(rmsnorm_bwd_kernel<V, W, N>, g, 32 * N, smem, s, d, lddy, xb, ldx, wb, rstd, rows, D, p.parts, o, lddx, sums)
+    e = launch_big<rmsnorm_bwd_kernel<V, W, N>>(g, 32 * N, smem, s, d, lddy, xb, ldx, wb, rstd, rows, D, p.parts, o, lddx, sums)
     // three 8-column pieces a thread: with the next row's in registers too, five
     // would spill (8192 x 5120 rows: 89 us, 54 us with three)
     if (p.w == 1) {
