@@ -119,7 +119,7 @@ struct BwdPlan {
     static constexpr int SEL_OFF = R_OFF + SLOTS * TILE;
     static constexpr int STAT_OFF = SEL_OFF + 2 * kStatBytes;
     static constexpr int BAR_OFF = DQ ? SEL_OFF + kTile * 4 : STAT_OFF + STATS * kStatBytes;
-    // a_full, raw0, raw1, s_full[2], d_full, e0, e1, done, drain, s_read, d_read, staged; full, empty [SLOTS]
+    // a_full, raw0, raw1, s_full[2], d_full, e0, e1 (dq: e0[2]), done, drain, s_read, d_read, staged; full, empty [SLOTS]
     static constexpr int NBARS = 13 + 2 * SLOTS;
     static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
     static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 ok = issue_s(j + 1) && warp_wait(m.d_read, j & 1, abort_flag) && issue_dp(j + 1);
                 if (!ok) break;
             }
-            if (!warp_wait(m.e0, j & 1, abort_flag)) { ok = false; break; }
+            if (!warp_wait(m.e0 + 8 * (j & 1), (j >> 1) & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             const int st = first(j).s;
             const uint32_t so = (st * P::TILE) >> 4;
@@ -534,7 +534,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(m.e0);
+            // two barriers in turn: dP_{j+1} does not wait for this tile's arrivals,
+            // so a warp may arrive for the next tile before another has for this one
+            if (lane == 0) mbar_arrive(m.e0 + 8 * (j & 1));
         }
         if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(m.done, 0, abort_flag));
         if (!ok) {

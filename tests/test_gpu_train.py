@@ -543,3 +543,23 @@ def test_gradient_through_the_attention_half_of_a_video_block():
     for name, got, want in (("o", o, O.detach()), ("dx", dx, X.grad), ("dmod", dmod, M.grad), ("dwq", dwq, WQ.grad), ("dwk", dwk, WK.grad)):
         rel = float((got.double() - want).norm() / want.norm())
         assert rel <= 10 * 2.0 ** -8, f"{name}: {rel:.3e}"
+
+
+@pytest.mark.parametrize("case", [(2, 16, 16, 72, 1024, 1024), (2, 10, 10, 128, 2000, 512), (2, 8, 2, 64, 1500, 1500, 1)],
+                         ids=lambda c: "x".join(map(str, c)))
+def test_attention_keeps_its_bits_over_many_calls(case):
+    """A wait that misses a phase, or an arrival counted for the wrong one, shows up rarely:
+    as other bits, or as the error word of a wait that ran out."""
+    p = Problem(*case)
+    grads = p.grads()
+    wf, wb = p.forward(), p.backward(grads)
+    torch.cuda.synchronize()
+    keep = [t.clone() for t in (p.o, p.lse, *grads)]
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(400):
+        p.forward(wf)
+        p.backward(grads, wb)
+        if i % 4 == 0:
+            for a, b in zip(keep, (p.o, p.lse, *grads)):
+                differ += (a != b).sum()
+    assert int(differ.item()) == 0 and int(p.err.item()) == 0
