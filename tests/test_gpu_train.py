@@ -27,6 +27,15 @@ F = 2.0 ** -18
 NAN = float("nan")
 
 
+@pytest.fixture(autouse=True)
+def float32_by_default():
+    """Another test module of the same process may have set another default."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 def stream():
     return torch.cuda.current_stream().cuda_stream
 
