@@ -17,18 +17,30 @@
 //
 // In both, dS (and P) is the A operand straight from tensor memory: the
 // thread that owns a TMEM lane (a query row, a key) reads 32 columns of the
-// fp32 product and writes their bf16 values over the columns it has read.  The
-// B operands of the accumulating products are the tiles already in shared
-// memory, read MN-major.  20 warps: 0 TMA, 1 MMA issue, 4..19 elementwise (four
-// per 32 TMEM lanes, each a quarter of the 128 columns).  The products of tile j + 1
-// that do not wait for the elementwise work of tile j are issued before those
-// that do, so the tensor core computes while the elementwise warps run.
+// fp32 product and writes their bf16 values.  The B operands of the accumulating
+// products are the tiles already in shared memory, read MN-major.  20 warps: 0
+// TMA, 1 and 2 MMA issue, 4..19 elementwise (four per 32 TMEM lanes, each a
+// quarter of the 128 columns).  A product's place is free as soon as it has been
+// read, so the next one runs while the elementwise warps work on it.
 //
-// dq_kernel also writes, for dkv_kernel, L (in units of log2, +inf where a row
-// sees nothing, which makes P = 0) and D, 128 of each per query tile.
+// What bounds it (measured on copies with parts left out, head dim 128): the
+// elementwise work is hidden (exponentials left out: same time), loads alone
+// take 0.77 us a tile of the dQ kernel, the products 1.2 us where their
+// instructions need 0.8 at 1.9 GHz; the tensor core is 53% (dQ) and 70% (dK, dV)
+// active over a whole launch, the rest is the start and end of each CTA (~6 us,
+// one CTA per SM) and waits between products.  Issue matters: from a branch of a
+// single thread an MMA takes ~48 cycles to issue, from a converged warp with
+// one elected lane <= 32, and a tile has 24 to 42 of them.
+//
+// dq_kernel also writes, for dkv_kernel, -L (in units of the raw score) and -D of
+// each query as three bf16 parts in an operand tile: dkv_kernel adds them with one
+// more K = 16 step of S^T and dP^T (against constant selecting rows), so its
+// threads, which own keys, need no per-query values.  (Reading them from shared
+// memory took ~1300 wavefronts a tile.)  A row that sees nothing
+// has -1e30, which makes P = 0.
 //
 // P and dS are rounded to bf16 as operands of the tensor core (relative 2^-8
-// at most, as P in the forward); every sum is fp32.  Every mbarrier wait is
+// at most each, as P in the forward); every sum is fp32.  Every mbarrier wait is
 // bounded; one that runs out sets the error word, all roles leave their
 // loops, loads and MMAs in flight are drained and TMEM is freed.
 #include "attention.cuh"
@@ -113,13 +125,19 @@ struct BwdPlan {
     static constexpr bool P_APART = FREE >= 64, DS_APART = FREE >= 128;
     static constexpr uint32_t P_COL = P_APART ? DK_COL + T::HDP : 0;
     static constexpr uint32_t DS_COL = DS_APART ? P_COL + 64 : 128;
+    // Issuing warps of dkv_kernel.  Two (S and dV; dP and dK) keep the tensor core
+    // fed while one waits: at head dim 64 (72) a tile takes 0.90 (1.11) us against
+    // 1.09 (1.27).  Where P and dS lie in the places of S and dP, each product
+    // has to wait for one of the other kind and the order of issue counts: one
+    // (head dim 128: 1.34 against 1.56).
+    static constexpr int ISSUERS = P_APART ? 2 : 1;
     static constexpr int A0_OFF = 0, A1_OFF = TILE;
     static constexpr int R_OFF = 2 * TILE;
     // dq: D of each row; dkv: the two selecting operands, then the statistics
     static constexpr int SEL_OFF = R_OFF + SLOTS * TILE;
     static constexpr int STAT_OFF = SEL_OFF + 2 * kStatBytes;
     static constexpr int BAR_OFF = DQ ? SEL_OFF + kTile * 4 : STAT_OFF + STATS * kStatBytes;
-    // a_full, raw0, raw1, s_full[2], d_full, e0, e1 (dq: e0[2]), done, drain, s_read, d_read, staged; full, empty [SLOTS]
+    // a_full, raw0, raw1, s_full, drain2, d_full, e0, e1, done, drain, s_read, d_read, staged; full, empty [SLOTS]
     static constexpr int NBARS = 13 + 2 * SLOTS;
     static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
     static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
@@ -133,33 +151,33 @@ struct BwdPlan {
 };
 
 struct BwdBars {
-    uint32_t a_full, raw0, raw1, s_full, d_full, e0, e1, done, drain, s_read, d_read, staged, full, empty;
+    uint32_t a_full, raw0, raw1, s_full, drain2, d_full, e0, e1, done, drain, s_read, d_read, staged, full, empty;
 };
 
 template <int SLOTS>
 __device__ __forceinline__ BwdBars bwd_bars(uint32_t b) {
-    return {b, b + 8, b + 16, b + 24, b + 40, b + 48, b + 56, b + 64, b + 72, b + 80, b + 88,
+    return {b, b + 8, b + 16, b + 24, b + 32, b + 40, b + 48, b + 56, b + 64, b + 72, b + 80, b + 88,
             b + 96, b + 104, b + 104 + 8 * SLOTS};
 }
 
 template <int SLOTS>
-__device__ __forceinline__ void bwd_init(const BwdBars& m) {
+__device__ __forceinline__ void bwd_init(const BwdBars& m, int done, int readers) {
     mbar_init(m.a_full, 1);
     mbar_init(m.raw0, 1);
     mbar_init(m.raw1, 1);
     mbar_init(m.s_full, 1);
-    mbar_init(m.s_full + 8, 1);
     mbar_init(m.d_full, 1);
     mbar_init(m.e0, 4 * kGroups);
     mbar_init(m.e1, 4 * kGroups);
     mbar_init(m.s_read, 4 * kGroups);
     mbar_init(m.d_read, 4 * kGroups);
     mbar_init(m.staged, 4 * kGroups);
-    mbar_init(m.done, 1);
+    mbar_init(m.done, done);
     mbar_init(m.drain, 1);
+    mbar_init(m.drain2, 1);
     for (int i = 0; i < SLOTS; ++i) {
         mbar_init(m.full + 8 * i, 1);
-        mbar_init(m.empty + 8 * i, 1);
+        mbar_init(m.empty + 8 * i, readers);
     }
     fence_mbar_init();
 }
@@ -266,6 +284,19 @@ __device__ __forceinline__ float dot8(uint4 a, uint4 b) {
     return t;
 }
 
+// The end of an issuing warp: on an abort, its MMAs in flight are waited for.
+template <typename Fail>
+__device__ __forceinline__ void end_issue(bool one, bool ok, uint32_t drain, const volatile int* abort_flag, const Fail& fail) {
+    if (one) {
+        if (!ok) fail();
+        if (*abort_flag) {
+            tc_commit(drain);
+            mbar_wait(drain, 0, nullptr);
+        }
+    }
+    __syncwarp();
+}
+
 // A raw score that no score makes up for: exp of it is 0, and times 0 it is 0.
 constexpr float kNothing = -1e30f;
 
@@ -280,9 +311,12 @@ __device__ __forceinline__ void write_stat(uint4* stat, int r, float neg_l, floa
 }
 
 // ------------------------------------------------------------------ dQ
-// TMEM: S in two buffers [0, 128) and [128, 256), dP [256, 384), dQ [384, 512).
-// Issue order S_0 dP_0 | S_1 . dP_1 dQ_0 | S_2 . dP_2 dQ_1 | ... where "." waits
-// for dS: dP_{j+1} goes before dQ_j because the elementwise warps wait for it.
+// TMEM: S [0, 128), dP [128, 256), dS [256, 320), dQ [384, 512).  Issue order
+// S_0 dP_0 | S_1 dP_1 dQ_0 | S_2 dP_2 dQ_1 | ...: S_{j+1} goes once S_j is read
+// and dP_{j+1} once dP_j is, both before the elementwise warps have formed dS_j,
+// so that they find their next operands ready.  Two warps issue, S and dP one, dQ
+// the other: each waits for its own barriers while the other's products run (a
+// tile at head dim 64: 0.74 us, against 0.84 with one).
 template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
@@ -327,7 +361,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // D = rowsum(dO O): LP lanes read one row's 16-byte pieces side by side, eight
     // rows a warp, all loads at once: they overlap the set-up.  (One row a lane
     // touches 32 rows a load instruction: set-up took 14000 cycles with 40 x 128
-    // columns a row, against @@.)
+    // columns a row, against 6200.)
     constexpr int LP = NB == 1 && !TAIL ? 8 : 16, RP = 32 / LP;
     float* row_d = reinterpret_cast<float*>(smem + P::SEL_OFF);
     uint4 o[8 / RP], d[8 / RP];
@@ -345,7 +379,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         if (i < qlen) l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
     }
     if (threadIdx.x == 0) {
-        bwd_init<P::SLOTS>(m);
+        bwd_init<P::SLOTS>(m, 1, 1);
         *abort_flag = 0;
         // this thread is also the one that loads: the first tiles need not wait
         // for the rest of the set-up
@@ -418,11 +452,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
         }
     } else if (warp == 1) {
-        // ---------------- MMA issuer: the warp waits, one lane issues
+        // ---------------- MMA issuer of S and dP: the warp waits, one lane issues
         const bool one = elect_one();
         const uint64_t q = sw128_kmajor_desc(sb + P::A0_OFF), qtl = sw32_desc(sb + P::A0_OFF + NB * T::BLK);
         const uint64_t d = sw128_kmajor_desc(sb + P::A1_OFF), dtl = sw32_desc(sb + P::A1_OFF + NB * T::BLK);
-        const uint64_t k = sw128_kmajor_desc(sb + P::R_OFF), kmn = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK);
+        const uint64_t k = sw128_kmajor_desc(sb + P::R_OFF);
         const uint64_t ktl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
         const uint64_t v = sw128_kmajor_desc(sb + P::R_OFF), vtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
         auto issue_s = [&](int j) -> bool {
@@ -431,8 +465,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
-                mma_scores<NB, TAIL>(tmem + (j & 1) * 128, q, qtl, k + so, ktl + so);
-                tc_commit(m.s_full + 8 * (j & 1));
+                mma_scores<NB, TAIL>(tmem, q, qtl, k + so, ktl + so);
+                tc_commit(m.s_full);
             }
             __syncwarp();
             return true;
@@ -443,7 +477,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
-                mma_scores<NB, TAIL>(tmem + 256, d, dtl, v + so, vtl + so);
+                mma_scores<NB, TAIL>(tmem + 128, d, dtl, v + so, vtl + so);
                 tc_commit(m.d_full);
                 tc_commit(m.empty + 8 * t.s);
             }
@@ -451,33 +485,29 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             return true;
         };
         bool ok = warp_wait(m.a_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
-        for (int j = 0; ok && j < n; ++j) {
-            if (j + 1 < n) {
-                // S_{j+1} overwrites dS_{j-1}, which dQ_{j-1}, issued before, reads
-                ok = issue_s(j + 1) && warp_wait(m.d_read, j & 1, abort_flag) && issue_dp(j + 1);
-                if (!ok) break;
-            }
-            if (!warp_wait(m.e0 + 8 * (j & 1), (j >> 1) & 1, abort_flag)) { ok = false; break; }
+        for (int j = 1; ok && j < n; ++j)
+            ok = warp_wait(m.s_read, (j - 1) & 1, abort_flag) && issue_s(j) && warp_wait(m.d_read, (j - 1) & 1, abort_flag) && issue_dp(j);
+        end_issue(one, ok, m.drain, abort_flag, fail);
+    } else if (warp == 2) {
+        // ---------------- MMA issuer of dQ
+        const bool one = elect_one();
+        const uint64_t k = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK), ktl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
+        bool ok = true;
+        for (int j = 0; j < n; ++j) {
+            const Slot t = first(j);
+            if (!warp_wait(m.full + 8 * t.s, t.ph, abort_flag) || !warp_wait(m.e0, j & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            const int st = first(j).s;
-            const uint32_t so = (st * P::TILE) >> 4;
+            const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
-                mma_accumulate<NB, TAIL, kCols>(tmem + 384, tmem + (j & 1) * 128, kmn + so, ktl + so, j == 0);
-                tc_commit(m.empty + 8 * st);
+                mma_accumulate<NB, TAIL, kCols / 2>(tmem + 384, tmem + 256, k + so, ktl + so, j == 0);
+                tc_commit(m.empty + 8 * t.s);
+                if (j + 1 == n) tc_commit(m.done);
             }
             __syncwarp();
         }
-        if (one) {
-            if (ok) tc_commit(m.done);
-            else fail();
-            if (*abort_flag) {
-                tc_commit(m.drain);
-                mbar_wait(m.drain, 0, nullptr);
-            }
-        }
-        __syncwarp();
+        end_issue(one, ok, m.drain2, abort_flag, fail);
     } else if (warp >= 4) {
-        // ---------------- elementwise: thread = query row, half of the columns
+        // ---------------- elementwise: thread = query row, a quarter of the columns
         const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;    // group, TMEM lane
         const int i = row0 + row;
         const int end = i < qlen ? key_end(i, off, g.causal_block, klen) : 0;
@@ -497,12 +527,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const uint64_t scale2 = f32x2(g.scale_log2, g.scale_log2), neg_l2 = f32x2(-l2, -l2), neg_d = f32x2(-delta, -delta);
         bool ok = true;
         for (int j = 0; j < n; ++j) {
-            const uint32_t ts = tl + (j & 1) * 128 + kCols * e;
-            if (!warp_wait(m.s_full + 8 * (j & 1), (j >> 1) & 1, abort_flag)) { ok = false; break; }
+            if (!warp_wait(m.s_full, j & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
             uint32_t r[32];
-            tmem_ld_32x32b_x32(ts, r);
+            tmem_ld_32x32b_x32(tl + kCols * e, r);
             tmem_wait_ld_r(r);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(m.s_read);
             float p[32];
 #pragma unroll
             for (int c = 0; c < 32; c += 2) {
@@ -512,7 +544,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
             if (!warp_wait(m.d_full, j & 1, abort_flag)) { ok = false; break; }
             tc_fence_after();
-            tmem_ld_32x32b_x32(tl + 256 + kCols * e, r);
+            tmem_ld_32x32b_x32(tl + 128 + kCols * e, r);
             tmem_wait_ld_r(r);
             tc_fence_before();
             __syncwarp();
@@ -530,13 +562,16 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             uint32_t w[16];
 #pragma unroll
             for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-            tmem_st_32x32b_x16(ts, w);
+            // the last reader of dS's columns, dQ_{j-1}, releases its K slot when done
+            if (j > 0) {
+                const Slot k = first(j - 1);
+                if (!warp_wait(m.empty + 8 * k.s, k.ph, abort_flag)) { ok = false; break; }
+            }
+            tmem_st_32x32b_x16(tl + 256 + kCols / 2 * e, w);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            // two barriers in turn: dP_{j+1} does not wait for this tile's arrivals,
-            // so a warp may arrive for the next tile before another has for this one
-            if (lane == 0) mbar_arrive(m.e0 + 8 * (j & 1));
+            if (lane == 0) mbar_arrive(m.e0);
         }
         if (ok) ok = __all_sync(0xFFFFFFFFu, mbar_wait(m.done, 0, abort_flag));
         if (!ok) {
@@ -576,10 +611,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 }
 
 // ------------------------------------------------------------------ dK, dV
-// TMEM: S^T [0, 128), dP^T [128, 256), dV [256, 384), dK [384, 512); P^T and
-// dS^T take the places of S^T and dP^T.  Issue order S_0 dP_0 | . dV_0 S_1 . dK_0
-// dP_1 | . dV_1 S_2 . dK_1 dP_2 | ...: dV_i and S_{i+1} run while the elementwise
-// warps form dS_i, dK_i and dP_{i+1} while they form P_{i+1}.
+// TMEM: S^T [0, 128), dP^T [128, 256), then dV, dK and, where they fit, P^T and
+// dS^T; else these take the places of S^T and dP^T, and then dV_i goes before
+// S_{i+1} and dK_i before dP_{i+1} in one order of issue.
 template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
@@ -627,7 +661,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
 
     if (threadIdx.x == 0) {
-        bwd_init<P::SLOTS>(m);
+        bwd_init<P::SLOTS>(m, P::ISSUERS, P::ISSUERS);
         *abort_flag = 0;
         mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
         load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, key0, b, m.a_full);
@@ -720,80 +754,121 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 in.drain<P::SLOTS>(m.full);
             }
         }
-    } else if (warp == 1) {
-        // ---------------- MMA issuer: the warp waits, one lane issues
+    } else if (warp == 1 || (P::ISSUERS == 2 && warp == 2)) {
+        // ---------------- MMA issuers: the warp waits, one lane issues
         const bool one = elect_one();
         const uint64_t k = sw128_kmajor_desc(sb + P::A0_OFF), ktl = sw32_desc(sb + P::A0_OFF + NB * T::BLK);
         const uint64_t v = sw128_kmajor_desc(sb + P::A1_OFF), vtl = sw32_desc(sb + P::A1_OFF + NB * T::BLK);
-        const uint64_t q = sw128_kmajor_desc(sb + P::R_OFF), qmn = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK);
-        const uint64_t qtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
-        const uint64_t d = sw128_kmajor_desc(sb + P::R_OFF), dmn = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK);
-        const uint64_t dtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
+        const uint64_t r = sw128_kmajor_desc(sb + P::R_OFF), rmn = sw128_mnmajor_desc(sb + P::R_OFF, T::BLK);
+        const uint64_t rtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
         const uint64_t sel = sw32_desc(sb + P::SEL_OFF), stat = sw32_desc(sb + P::STAT_OFF);
-        auto issue_s = [&](int i) -> bool {
+        constexpr uint32_t id = idesc_bf16_f32(kTile, kTile);
+        const auto full = [&](Slot t) { return warp_wait(m.full + 8 * t.s, t.ph, abort_flag); };
+        // a slot is free when both products that read it are done: with one
+        // issuer the later one's completion says so, with two each says its own
+        const auto issue_s = [&](int i) -> bool {
             const Slot t = first(i);
-            if (!warp_wait(m.full + 8 * t.s, t.ph, abort_flag)) return false;
+            if (!full(t)) return false;
             tc_fence_after();
             const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
-                mma_scores<NB, TAIL>(tmem, k, ktl, q + so, qtl + so);
-                tc_mma_f16(tmem, sel, stat + ((i % P::STATS * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
+                mma_scores<NB, TAIL>(tmem, k, ktl, r + so, rtl + so);
+                tc_mma_f16(tmem, sel, stat + ((i % P::STATS * kStatBytes) >> 4), id, 1u);
                 tc_commit(m.s_full);
+                if (P::ISSUERS == 2) tc_commit(m.empty + 8 * t.s);
             }
             __syncwarp();
             return true;
         };
-        auto issue_dp = [&](int i) -> bool {
+        const auto issue_dp = [&](int i) -> bool {
             const Slot t = second(i);
-            if (!warp_wait(m.full + 8 * t.s, t.ph, abort_flag)) return false;
+            // the statistics came with Q_i; one issuer has waited for it
+            if ((P::ISSUERS == 2 && !full(first(i))) || !full(t)) return false;
             tc_fence_after();
             const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
-                mma_scores<NB, TAIL>(tmem + 128, v, vtl, d + so, dtl + so);
-                // the statistics came with Q_i, which S_i has waited for
-                tc_mma_f16(tmem + 128, sel + (kStatBytes >> 4), stat + ((i % P::STATS * kStatBytes) >> 4), idesc_bf16_f32(kTile, kTile), 1u);
+                mma_scores<NB, TAIL>(tmem + 128, v, vtl, r + so, rtl + so);
+                tc_mma_f16(tmem + 128, sel + (kStatBytes >> 4), stat + ((i % P::STATS * kStatBytes) >> 4), id, 1u);
                 tc_commit(m.d_full);
+                if (P::ISSUERS == 2) tc_commit(m.empty + 8 * t.s);
             }
             __syncwarp();
             return true;
         };
-        bool ok = warp_wait(m.a_full, 0, abort_flag) && issue_s(0) && issue_dp(0);
-        for (int i = 0; ok && i < n; ++i) {
-            const int st = first(i).s, sd = second(i).s;
-            const uint32_t so = (st * P::TILE) >> 4, sdo = (sd * P::TILE) >> 4;
-            const bool more = i + 1 < n;
+        const auto issue_dv = [&](int i) -> bool {
+            const Slot t = second(i);
+            if (!full(t) || !warp_wait(m.e0, i & 1, abort_flag)) return false;
+            tc_fence_after();
+            const uint32_t so = (t.s * P::TILE) >> 4;
+            if (one) {
+                mma_accumulate<NB, TAIL, P::P_APART ? kCols / 2 : kCols>(tmem + P::DV_COL, tmem + P::P_COL, rmn + so, rtl + so, i == 0);
+                tc_commit(m.empty + 8 * t.s);
+                if (i + 1 == n) tc_commit(m.done);
+            }
+            __syncwarp();
+            return true;
+        };
+        const auto issue_dk = [&](int i) -> bool {
+            const Slot t = first(i);
+            if (!warp_wait(m.e1, i & 1, abort_flag)) return false;
+            tc_fence_after();
+            const uint32_t so = (t.s * P::TILE) >> 4;
+            if (one) {
+                mma_accumulate<NB, TAIL, P::DS_APART ? kCols / 2 : kCols>(tmem + P::DK_COL, tmem + P::DS_COL, rmn + so, rtl + so, i == 0);
+                tc_commit(m.empty + 8 * t.s);
+                if (i + 1 == n) tc_commit(m.done);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = warp_wait(m.a_full, 0, abort_flag);
+        if constexpr (P::ISSUERS == 1) {
+            // written out: through the four calls below a tile takes 6% longer
+            ok = ok && issue_s(0) && issue_dp(0);
+            for (int i = 0; ok && i < n; ++i) {
+                const int st = first(i).s, sd = second(i).s;
+                const uint32_t so = (st * P::TILE) >> 4, sdo = (sd * P::TILE) >> 4;
+                const bool more = i + 1 < n;
+                if (!warp_wait(m.e0, i & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                if (one) {
+                    mma_accumulate<NB, TAIL, kCols>(tmem + P::DV_COL, tmem + P::P_COL, rmn + sdo, rtl + sdo, i == 0);
+                    tc_commit(m.empty + 8 * sd);
+                }
+                __syncwarp();
+                if (more && !issue_s(i + 1)) { ok = false; break; }
+                if (!warp_wait(m.e1, i & 1, abort_flag)) { ok = false; break; }
+                tc_fence_after();
+                if (one) {
+                    mma_accumulate<NB, TAIL, kCols>(tmem + P::DK_COL, tmem + P::DS_COL, rmn + so, rtl + so, i == 0);
+                    tc_commit(m.empty + 8 * st);
+                }
+                __syncwarp();
+                if (more && !issue_dp(i + 1)) { ok = false; break; }
+            }
+            if (one && ok) tc_commit(m.done);
+        } else if (warp == 1) {
             // S_{i+1} takes S_i's place once that is read; where P_i lies there, after dV_i
-            if (P::P_APART && more && !(warp_wait(m.s_read, i & 1, abort_flag) && issue_s(i + 1))) { ok = false; break; }
-            if (!warp_wait(m.e0, i & 1, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            if (one) {
-                mma_accumulate<NB, TAIL, P::P_APART ? kCols / 2 : kCols>(tmem + P::DV_COL, tmem + P::P_COL, dmn + sdo, dtl + sdo, i == 0);
-                tc_commit(m.empty + 8 * sd);
+            ok = ok && issue_s(0);
+            for (int i = 0; ok && i < n; ++i) {
+                const bool more = i + 1 < n;
+                if (P::P_APART && more) ok = warp_wait(m.s_read, i & 1, abort_flag) && issue_s(i + 1);
+                ok = ok && issue_dv(i);
+                if (!P::P_APART && more) ok = ok && issue_s(i + 1);
             }
-            __syncwarp();
-            if (!P::P_APART && more && !issue_s(i + 1)) { ok = false; break; }
+        } else {
             // likewise dP_{i+1}, dS_i and dK_i
-            if (P::DS_APART && more && !(warp_wait(m.d_read, i & 1, abort_flag) && issue_dp(i + 1))) { ok = false; break; }
-            if (!warp_wait(m.e1, i & 1, abort_flag)) { ok = false; break; }
-            tc_fence_after();
-            if (one) {
-                mma_accumulate<NB, TAIL, P::DS_APART ? kCols / 2 : kCols>(tmem + P::DK_COL, tmem + P::DS_COL, qmn + so, qtl + so, i == 0);
-                tc_commit(m.empty + 8 * st);
-            }
-            __syncwarp();
-            if (!P::DS_APART && more && !issue_dp(i + 1)) { ok = false; break; }
-        }
-        if (one) {
-            if (ok) tc_commit(m.done);
-            else fail();
-            if (*abort_flag) {
-                tc_commit(m.drain);
-                mbar_wait(m.drain, 0, nullptr);
+            ok = ok && issue_dp(0);
+            for (int i = 0; ok && i < n; ++i) {
+                const bool more = i + 1 < n;
+                if (P::DS_APART && more) ok = warp_wait(m.d_read, i & 1, abort_flag) && issue_dp(i + 1);
+                ok = ok && issue_dk(i);
+                if (!P::DS_APART && more) ok = ok && issue_dp(i + 1);
             }
         }
-        __syncwarp();
+        end_issue(one, ok, warp == 1 ? m.drain : m.drain2, abort_flag, fail);
     } else if (warp >= 4) {
-        // ---------------- elementwise: thread = key, half of the query columns
+        // ---------------- elementwise: thread = key, a quarter of the query columns
         const int e = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;    // group, TMEM lane
         const int key = key0 + row;
         const int begin = key < klen ? query_begin(key, off, g.causal_block) : 1 << 30;   // queries that see it: [begin, qlen)
@@ -960,7 +1035,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ J
 //     or more to a CTA.
 //   dK, dV: likewise over the group's query tiles; with a causal mask also
 //     where the longest CTA (all query tiles) has more than an SM's share of
-//     the whole (3 sequences of 2047 tokens, 16 heads over 4: @@ us unsplit, @@ in two).
+//     the whole (3 sequences of 2047 tokens, 16 heads over 4: 109 us unsplit, 96 in two).
 struct BwdSplit {
     int q, k;
     size_t part_q, part_k, part_v, total;      // byte offsets
