@@ -334,6 +334,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         const int row = q * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(q * 32) << 16);
         float m_ref = -INFINITY, l = 0.f;
+        const uint64_t scale2 = f32x2(scale_log2, scale_log2);
         bool ok = true;
         int row_end = nk;         // one past the last key of this row
         if constexpr (TR) {
@@ -383,9 +384,11 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             const float neg = TR && m_new == -INFINITY ? 0.f : -m_new;
             float sp[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < TK; ++i) {
-                v[i] = ex2_approx(fmaf(v[i], scale_log2, neg));
-                sp[i & 7] += v[i];
+            for (int i = 0; i < TK; i += 2) {
+                f32x2_split(fma_f32x2(f32x2(v[i], v[i + 1]), scale2, f32x2(neg, neg)), v[i], v[i + 1]);
+                v[i] = ex2_approx(v[i]);
+                v[i + 1] = ex2_approx(v[i + 1]);
+                f32x2_split(add_f32x2(f32x2(sp[i & 7], sp[(i & 7) + 1]), f32x2(v[i], v[i + 1])), sp[i & 7], sp[(i & 7) + 1]);
             }
             const float rs = ((sp[0] + sp[1]) + (sp[2] + sp[3])) + ((sp[4] + sp[5]) + (sp[6] + sp[7]));
             l = l * corr + rs;
