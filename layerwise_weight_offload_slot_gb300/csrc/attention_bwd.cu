@@ -81,9 +81,8 @@ struct BwdArgs {
     int* err;
 };
 
-// Shared memory of one CTA: two tiles that stay (Q and dO; K and V), two
-// rings that move (K and V; Q and dO), operand tiles for bf16 dS and P, and
-// per-row statistics.  DQ: the plan of dq_kernel.
+// Shared memory of one CTA: two tiles that stay (Q and dO; K and V), slots for the
+// two streams of tiles that move (K and V; Q and dO), and per-row values.
 //
 // A reload takes ~1 us (2000 cycles) from L2, longer than an iteration's
 // products.  Tile i of the first stream (K in dq_kernel, Q in dkv_kernel) is
@@ -117,20 +116,6 @@ struct BwdPlan {
     static constexpr bool SHARED = NB == 2;
     static constexpr int SLOTS = SHARED ? (DQ ? 5 : 4) : 6;
     static constexpr int STATS = SHARED ? 2 : 3;            // statistics operands of dkv_kernel, tile i in i % STATS
-    // dkv_kernel's tensor memory: S^T [0, 128), dP^T [128, 256), then dV and dK, then P^T
-    // and dS^T (64 columns each) where 512 columns hold them.  A P or dS that
-    // takes the place of its product instead makes the next product wait for it.
-    static constexpr uint32_t DV_COL = 256, DK_COL = DV_COL + T::HDP;
-    static constexpr uint32_t FREE = 512 - DK_COL - T::HDP;
-    static constexpr bool P_APART = FREE >= 64, DS_APART = FREE >= 128;
-    static constexpr uint32_t P_COL = P_APART ? DK_COL + T::HDP : 0;
-    static constexpr uint32_t DS_COL = DS_APART ? P_COL + 64 : 128;
-    // Issuing warps of dkv_kernel.  Two (S and dV; dP and dK) keep the tensor core
-    // fed while one waits: at head dim 64 (72) a tile takes 0.90 (1.11) us against
-    // 1.09 (1.27).  Where P and dS lie in the places of S and dP, each product
-    // has to wait for one of the other kind and the order of issue counts: one
-    // (head dim 128: 1.34 against 1.56).
-    static constexpr int ISSUERS = P_APART ? 2 : 1;
     static constexpr int A0_OFF = 0, A1_OFF = TILE;
     static constexpr int R_OFF = 2 * TILE;
     // dq: D of each row; dkv: the two selecting operands, then the statistics
@@ -147,7 +132,25 @@ struct BwdPlan {
     static constexpr int WANT = USED + 1024 > 118784 ? USED + 1024 : 118784;
     static constexpr int BYTES = WANT < 227 * 1024 ? WANT : 227 * 1024;
     static_assert(USED <= 227 * 1024, "attention backward shared memory plan exceeds 227 KB");
-    static_assert(DK_COL + T::HDP <= 512, "attention backward tensor memory plan");
+};
+
+// dkv_kernel's tensor memory: S^T [0, 128), dP^T [128, 256), then dV and dK, then P^T
+// and dS^T (64 columns each) where 512 columns hold them.  A P or dS that
+// takes the place of its product instead makes the next product wait for it.
+template <int HDP>
+struct DkvTmem {
+    static constexpr uint32_t DV_COL = 256, DK_COL = DV_COL + HDP;
+    static constexpr uint32_t FREE = 512 - DK_COL - HDP;
+    static constexpr bool P_APART = FREE >= 64, DS_APART = FREE >= 128;
+    static constexpr uint32_t P_COL = P_APART ? DK_COL + HDP : 0;
+    static constexpr uint32_t DS_COL = DS_APART ? P_COL + 64 : 128;
+    // Issuing warps of dkv_kernel.  Two (S and dV; dP and dK) keep the tensor core
+    // fed while one waits: at head dim 64 (72) a tile takes 0.90 (1.11) us against
+    // 1.09 (1.27).  Where P and dS lie in the places of S and dP, each product
+    // has to wait for one of the other kind and the order of issue counts: one
+    // (head dim 128: 1.34 against 1.56).
+    static constexpr int ISSUERS = P_APART ? 2 : 1;
+    static_assert(DK_COL + HDP <= 512, "attention backward tensor memory plan");
 };
 
 struct BwdBars {
@@ -619,6 +622,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
     using P = BwdPlan<NB, TAIL, false>;
     using T = AttnTile<NB, TAIL>;
+    using M = DkvTmem<T::HDP>;
     const auto first = [](int i) { return slot_of<P::SLOTS, P::SHARED, false>(i); };
     const auto second = [](int i) { return slot_of<P::SLOTS, P::SHARED, true>(i); };
     extern __shared__ uint8_t smem_raw[];
@@ -661,7 +665,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     }
 
     if (threadIdx.x == 0) {
-        bwd_init<P::SLOTS>(m, P::ISSUERS, P::ISSUERS);
+        bwd_init<P::SLOTS>(m, M::ISSUERS, M::ISSUERS);
         *abort_flag = 0;
         mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
         load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, key0, b, m.a_full);
@@ -754,7 +758,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 in.drain<P::SLOTS>(m.full);
             }
         }
-    } else if (warp == 1 || (P::ISSUERS == 2 && warp == 2)) {
+    } else if (warp == 1 || (M::ISSUERS == 2 && warp == 2)) {
         // ---------------- MMA issuers: the warp waits, one lane issues
         const bool one = elect_one();
         const uint64_t k = sw128_kmajor_desc(sb + P::A0_OFF), ktl = sw32_desc(sb + P::A0_OFF + NB * T::BLK);
@@ -775,7 +779,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 mma_scores<NB, TAIL>(tmem, k, ktl, r + so, rtl + so);
                 tc_mma_f16(tmem, sel, stat + ((i % P::STATS * kStatBytes) >> 4), id, 1u);
                 tc_commit(m.s_full);
-                if (P::ISSUERS == 2) tc_commit(m.empty + 8 * t.s);
+                if (M::ISSUERS == 2) tc_commit(m.empty + 8 * t.s);
             }
             __syncwarp();
             return true;
@@ -783,14 +787,14 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const auto issue_dp = [&](int i) -> bool {
             const Slot t = second(i);
             // the statistics came with Q_i; one issuer has waited for it
-            if ((P::ISSUERS == 2 && !full(first(i))) || !full(t)) return false;
+            if ((M::ISSUERS == 2 && !full(first(i))) || !full(t)) return false;
             tc_fence_after();
             const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
                 mma_scores<NB, TAIL>(tmem + 128, v, vtl, r + so, rtl + so);
                 tc_mma_f16(tmem + 128, sel + (kStatBytes >> 4), stat + ((i % P::STATS * kStatBytes) >> 4), id, 1u);
                 tc_commit(m.d_full);
-                if (P::ISSUERS == 2) tc_commit(m.empty + 8 * t.s);
+                if (M::ISSUERS == 2) tc_commit(m.empty + 8 * t.s);
             }
             __syncwarp();
             return true;
@@ -801,7 +805,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
-                mma_accumulate<NB, TAIL, P::P_APART ? kCols / 2 : kCols>(tmem + P::DV_COL, tmem + P::P_COL, rmn + so, rtl + so, i == 0);
+                mma_accumulate<NB, TAIL, M::P_APART ? kCols / 2 : kCols>(tmem + M::DV_COL, tmem + M::P_COL, rmn + so, rtl + so, i == 0);
                 tc_commit(m.empty + 8 * t.s);
                 if (i + 1 == n) tc_commit(m.done);
             }
@@ -814,7 +818,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             const uint32_t so = (t.s * P::TILE) >> 4;
             if (one) {
-                mma_accumulate<NB, TAIL, P::DS_APART ? kCols / 2 : kCols>(tmem + P::DK_COL, tmem + P::DS_COL, rmn + so, rtl + so, i == 0);
+                mma_accumulate<NB, TAIL, M::DS_APART ? kCols / 2 : kCols>(tmem + M::DK_COL, tmem + M::DS_COL, rmn + so, rtl + so, i == 0);
                 tc_commit(m.empty + 8 * t.s);
                 if (i + 1 == n) tc_commit(m.done);
             }
@@ -822,7 +826,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             return true;
         };
         bool ok = warp_wait(m.a_full, 0, abort_flag);
-        if constexpr (P::ISSUERS == 1) {
+        if constexpr (M::ISSUERS == 1) {
             // written out: through the four calls below a tile takes 6% longer
             ok = ok && issue_s(0) && issue_dp(0);
             for (int i = 0; ok && i < n; ++i) {
@@ -832,7 +836,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 if (!warp_wait(m.e0, i & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (one) {
-                    mma_accumulate<NB, TAIL, kCols>(tmem + P::DV_COL, tmem + P::P_COL, rmn + sdo, rtl + sdo, i == 0);
+                    mma_accumulate<NB, TAIL, kCols>(tmem + M::DV_COL, tmem + M::P_COL, rmn + sdo, rtl + sdo, i == 0);
                     tc_commit(m.empty + 8 * sd);
                 }
                 __syncwarp();
@@ -840,7 +844,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 if (!warp_wait(m.e1, i & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 if (one) {
-                    mma_accumulate<NB, TAIL, kCols>(tmem + P::DK_COL, tmem + P::DS_COL, rmn + so, rtl + so, i == 0);
+                    mma_accumulate<NB, TAIL, kCols>(tmem + M::DK_COL, tmem + M::DS_COL, rmn + so, rtl + so, i == 0);
                     tc_commit(m.empty + 8 * st);
                 }
                 __syncwarp();
@@ -852,18 +856,18 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             ok = ok && issue_s(0);
             for (int i = 0; ok && i < n; ++i) {
                 const bool more = i + 1 < n;
-                if (P::P_APART && more) ok = warp_wait(m.s_read, i & 1, abort_flag) && issue_s(i + 1);
+                if (M::P_APART && more) ok = warp_wait(m.s_read, i & 1, abort_flag) && issue_s(i + 1);
                 ok = ok && issue_dv(i);
-                if (!P::P_APART && more) ok = ok && issue_s(i + 1);
+                if (!M::P_APART && more) ok = ok && issue_s(i + 1);
             }
         } else {
             // likewise dP_{i+1}, dS_i and dK_i
             ok = ok && issue_dp(0);
             for (int i = 0; ok && i < n; ++i) {
                 const bool more = i + 1 < n;
-                if (P::DS_APART && more) ok = warp_wait(m.d_read, i & 1, abort_flag) && issue_dp(i + 1);
+                if (M::DS_APART && more) ok = warp_wait(m.d_read, i & 1, abort_flag) && issue_dp(i + 1);
                 ok = ok && issue_dk(i);
-                if (!P::DS_APART && more) ok = ok && issue_dp(i + 1);
+                if (!M::DS_APART && more) ok = ok && issue_dp(i + 1);
             }
         }
         end_issue(one, ok, warp == 1 ? m.drain : m.drain2, abort_flag, fail);
@@ -887,7 +891,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             float p[32];
             tmem_ld_32x32b_x32(ts, r);
             tmem_wait_ld_r(r);
-            if constexpr (P::P_APART) {
+            if constexpr (M::P_APART) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m.s_read);
@@ -906,11 +910,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
 #pragma unroll
             for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-            if constexpr (P::P_APART) {
+            if constexpr (M::P_APART) {
                 // the last reader of its columns, dV_{i-1}, releases its dO slot when done
                 const Slot t = second(i - 1);
                 if (i > 0 && !warp_wait(m.empty + 8 * t.s, t.ph, abort_flag)) { ok = false; break; }
-                tmem_st_32x32b_x16(tl + P::P_COL + kCols / 2 * e, w);
+                tmem_st_32x32b_x16(tl + M::P_COL + kCols / 2 * e, w);
             } else {
                 tmem_st_32x32b_x16(ts, w);
             }
@@ -922,7 +926,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             tmem_ld_32x32b_x32(ts + 128, r);
             tmem_wait_ld_r(r);
-            if constexpr (P::DS_APART) {
+            if constexpr (M::DS_APART) {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m.d_read);
@@ -938,11 +942,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
 #pragma unroll
             for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
-            if constexpr (P::DS_APART) {
+            if constexpr (M::DS_APART) {
                 // the last reader of its columns, dK_{i-1}, releases its Q slot when done
                 const Slot t = first(i - 1);
                 if (i > 0 && !warp_wait(m.empty + 8 * t.s, t.ph, abort_flag)) { ok = false; break; }
-                tmem_st_32x32b_x16(tl + P::DS_COL + kCols / 2 * e, w);
+                tmem_st_32x32b_x16(tl + M::DS_COL + kCols / 2 * e, w);
             } else {
                 tmem_st_32x32b_x16(ts + 128, w);
             }
@@ -959,7 +963,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             // even groups bring dV, odd ones dK, into the first two slots
             const bool k = e & 1;
             float* part = parts ? (k ? g.part_k : g.part_v) + part_at + static_cast<size_t>(row) * ldp : nullptr;
-            store_row<NB, TAIL>(tl + (k ? P::DK_COL : P::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < g.nk,
+            store_row<NB, TAIL>(tl + (k ? M::DK_COL : M::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < g.nk,
                                 k ? g.scale : 1.f, e >> 1, kGroups / 2);
             if (!parts) {
                 fence_proxy_async_smem();

@@ -62,14 +62,11 @@ __device__ __forceinline__ void row_totals(float& v0, float& v1, float (*red)[2]
     }
 }
 
-// 16 (or 8) bytes from global to this thread's own place in shared memory, zeros
+// 16 bytes from global to this thread's own place in shared memory, zeros
 // where `in` is false; no barrier is needed between a thread's copies and its
 // reads of them, only its own wait.
 __device__ __forceinline__ void copy16(void* dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy8(void* dst, const void* src, bool in) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(in ? 8 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
