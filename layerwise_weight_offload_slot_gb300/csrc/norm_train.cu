@@ -77,6 +77,50 @@ __device__ __forceinline__ void copies_wait() {
 // What multiplies dy before the row sums: nothing, w (bf16) or 1 + scale (fp32)
 enum { kGainOne = 0, kGainW = 1, kGainScale = 2 };
 
+// Few rows: the column sums of 32 columns of one batch by one CTA, which reads
+// those columns of dy and x again (from L2), in the launch that forms dx.  32 row
+// groups of 8 lanes; each adds every 32nd row, then the groups are added in order.
+struct ColumnWork {
+    int first;                 // CTAs from this one on do columns
+    int slabs;                 // of 32 columns
+    float *out1, *out2;        // sum dy, sum dy xh
+    int ld;
+};
+
+__device__ __forceinline__ void column_slab(const ColumnWork& cw, const __nv_bfloat16* dy, const float* x, const float* mean,
+                                            const float* rstd, int rows, int D, int rpb, float4 (*sh)[8]) {
+    const int id = blockIdx.x - cw.first, b = id / cw.slabs, slab = id - b * cw.slabs;
+    const int rg = threadIdx.x >> 3, i = slab * 8 + (threadIdx.x & 7);      // row group, float4 of the row
+    const int row0 = b * rpb, n = min(rpb, rows - row0), n4 = D >> 2;
+    float4 s1 = make_float4(0.f, 0.f, 0.f, 0.f), s2 = s1;
+    if (i < n4) {
+#pragma unroll 8
+        for (int r = rg; r < n; r += 32) {
+            const size_t row = static_cast<size_t>(row0) + r;
+            const float4 v = reinterpret_cast<const float4*>(x + row * D)[i], d = bf4(reinterpret_cast<const uint2*>(dy + row * D)[i]);
+            const float mu = mean[row], rs = rstd[row];
+            s1 = make_float4(s1.x + d.x, s1.y + d.y, s1.z + d.z, s1.w + d.w);
+            s2 = make_float4(s2.x + d.x * ((v.x - mu) * rs), s2.y + d.y * ((v.y - mu) * rs), s2.z + d.z * ((v.z - mu) * rs),
+                             s2.w + d.w * ((v.w - mu) * rs));
+        }
+    }
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        sh[rg][threadIdx.x & 7] = which ? s2 : s1;
+        __syncthreads();
+        if (threadIdx.x < 8 && i < n4) {
+            float4 t = sh[0][threadIdx.x];
+#pragma unroll
+            for (int k = 1; k < 32; ++k) {
+                const float4 u = sh[k][threadIdx.x];
+                t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
+            }
+            reinterpret_cast<float4*>((which ? cw.out2 : cw.out1) + static_cast<size_t>(b) * cw.ld)[i] = t;
+        }
+        __syncthreads();
+    }
+}
+
 // One CTA: rows first, first + step, ... of one batch.  Column c of the row
 // belongs to the thread whose index within the row's warps is (c / 4) % (32 W).
 template <int V4, int W, int WARPS>
@@ -84,12 +128,19 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
     layernorm_bwd_kernel(const __nv_bfloat16* dy, const float* x, const float* __restrict__ mean,
                          const float* __restrict__ rstd, int rows, int D, int rpb, int parts, int gain_kind,
                          const void* __restrict__ gain, int gain_ld, const float* dres, float* dx,
-                         float* __restrict__ sum_dy, float* __restrict__ sum_dyxh, size_t sum_ld) {
+                         float* __restrict__ sum_dy, float* __restrict__ sum_dyxh, size_t sum_ld, const ColumnWork cw) {
     constexpr int R = WARPS / W;
     extern __shared__ float4 sh[];                  // [R][2][n4] when R > 1
     __shared__ float red[2][2][WARPS];
     pdl_wait();
     pdl_launch_dependents();
+    if constexpr (WARPS == 8) {
+        if (static_cast<int>(blockIdx.x) >= cw.first) {
+            __shared__ float4 cols[32][8];
+            column_slab(cw, dy, x, mean, rstd, rows, D, rpb, cols);
+            return;
+        }
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int b = blockIdx.x / parts, part = blockIdx.x - b * parts;
     const int rg = warp / W, t0 = (warp % W) * 32 + lane;
@@ -206,18 +257,60 @@ __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
 // next step, when every value read from it has been used, the others in flight.
 __host__ __device__ constexpr int ring_rows(int warps) { return warps == 32 ? 2 : 4; }
 
+// As column_slab, 64 columns of dw: the sum of dy xh.
+__device__ __forceinline__ void column_slab_rms(const ColumnWork& cw, const __nv_bfloat16* dy, int lddy, const __nv_bfloat16* x, int ldx,
+                                                const float* rstd, int rows, int D, float4 (*sh)[16]) {
+    const int slab = blockIdx.x - cw.first, rg = threadIdx.x >> 3, i = slab * 8 + (threadIdx.x & 7), n8 = D >> 3;
+    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (i < n8) {
+#pragma unroll 8
+        for (int r = rg; r < rows; r += 32) {
+            const uint4 xv = reinterpret_cast<const uint4*>(x + static_cast<size_t>(r) * ldx)[i];
+            const uint4 dv = reinterpret_cast<const uint4*>(dy + static_cast<size_t>(r) * lddy)[i];
+            const float rs = rstd[r];
+            const uint32_t xa[4] = {xv.x, xv.y, xv.z, xv.w}, da[4] = {dv.x, dv.y, dv.z, dv.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 xx = bf2(xa[k]), dd = bf2(da[k]);
+                s[2 * k] += dd.x * (xx.x * rs);
+                s[2 * k + 1] += dd.y * (xx.y * rs);
+            }
+        }
+    }
+    sh[rg][2 * (threadIdx.x & 7)] = make_float4(s[0], s[1], s[2], s[3]);
+    sh[rg][2 * (threadIdx.x & 7) + 1] = make_float4(s[4], s[5], s[6], s[7]);
+    __syncthreads();
+    const int c = slab * 16 + threadIdx.x;          // float4 of dw
+    if (threadIdx.x < 16 && c < 2 * n8) {
+        float4 t = sh[0][threadIdx.x];
+#pragma unroll
+        for (int k = 1; k < 32; ++k) {
+            const float4 u = sh[k][threadIdx.x];
+            t = make_float4(t.x + u.x, t.y + u.y, t.z + u.z, t.w + u.w);
+        }
+        reinterpret_cast<float4*>(cw.out1)[c] = t;
+    }
+}
+
 // RMSNorm backward on bf16 rows of strides ldy, ldx, lddx: dx may be dy or x
 // (each element is read by the thread that writes it, before it writes).
 template <int V8, int W, int WARPS>
 __global__ void __launch_bounds__(32 * WARPS, WARPS >= 32 ? 1 : 16 / WARPS)
     rmsnorm_bwd_kernel(const __nv_bfloat16* dy, int lddy, const __nv_bfloat16* x, int ldx,
                        const __nv_bfloat16* __restrict__ w, const float* __restrict__ rstd, int rows, int D, int parts,
-                       __nv_bfloat16* dx, int lddx, float* __restrict__ sums) {
+                       __nv_bfloat16* dx, int lddx, float* __restrict__ sums, const ColumnWork cw) {
     constexpr int R = WARPS / W;
     extern __shared__ float4 sh[];                  // the ring; at the end [R][D / 4] when R > 1
     __shared__ float red[2][2][WARPS];
     pdl_wait();
     pdl_launch_dependents();
+    if constexpr (WARPS == 8) {
+        if (static_cast<int>(blockIdx.x) >= cw.first) {
+            __shared__ float4 cols[32][16];
+            column_slab_rms(cw, dy, lddy, x, ldx, rstd, rows, D, cols);
+            return;
+        }
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rg = warp / W, t0 = (warp % W) * 32 + lane;
     const int n8 = D >> 3;
@@ -479,18 +572,32 @@ cudaError_t launch_layernorm_bwd(const void* dy, const float* x, const float* me
     const void* gain = scale ? static_cast<const void*>(scale) : w;
     // one CTA a batch writes its sums in place, several write partial rows
     const bool direct = p.parts == 1;
-    float* sums = !dshift ? nullptr : direct ? dshift : ws;
+    // The sums in the same launch where that is short: at most 2048 rows a slab
+    // (64 rows in a row a thread), at most 128 slabs.  In a graph, against the
+    // partial rows and their own launch: 1 x 256 x 256 2.2 us (3.9), 2 x 1024 x
+    // 1152 7.7 (9.6), 1 x 2048 x 4096 (128 slabs) 30.3 (31.5), but 4 x 1024 x 1152
+    // (144) 16.3 (13.6).
+    const int slabs = (D + 31) / 32;
+    const bool fused = dshift && !direct && p.warps == 8 && rpb <= 2048 && p.batches * slabs <= 128;
+    int parts = p.parts;
+    if (fused) {
+        const long long room = (2 * kGb300Sms - p.batches * slabs) / p.batches;
+        if (parts > room) parts = static_cast<int>(room < 1 ? 1 : room);
+    }
+    float* sums = !dshift || fused ? nullptr : direct ? dshift : ws;
     float* sums2 = !dshift ? nullptr : direct ? dscale : ws + D;
     const size_t sum_ld = direct ? static_cast<size_t>(dmod_ld) : 2 * static_cast<size_t>(D);
     const int r = p.warps / p.w;
     const size_t smem = sums && r > 1 ? static_cast<size_t>(r) * 2 * D * sizeof(float) : 0;
-    const unsigned g = static_cast<unsigned>(p.batches * p.parts);
+    const int row_ctas = static_cast<int>(p.batches * parts);
+    const ColumnWork cw = {row_ctas, slabs, dshift, dscale, dmod_ld};
+    const unsigned g = static_cast<unsigned>(row_ctas + (fused ? p.batches * slabs : 0));
     const __nv_bfloat16* d = static_cast<const __nv_bfloat16*>(dy);
     cudaError_t e = cudaErrorInvalidValue;
     const int v4 = (D / 4 + 32 * p.w - 1) / (32 * p.w);
 #define DLO_LNB(V, W, N)                                                                                          \
-    e = launch_k(layernorm_bwd_kernel<V, W, N>, g, 32 * N, smem, s, d, x, mean, rstd, rows, D, rpb, p.parts, kind, \
-                 gain, mod_ld, dres, dx, sums, sums2, sum_ld)
+    e = launch_k(layernorm_bwd_kernel<V, W, N>, g, 32 * N, smem, s, d, x, mean, rstd, rows, D, rpb, parts, kind, \
+                 gain, mod_ld, dres, dx, sums, sums2, sum_ld, cw)
     if (p.w == 1) {
         if (v4 <= 1) DLO_LNB(1, 1, 8);
         else if (v4 <= 3) DLO_LNB(3, 1, 8);
@@ -522,19 +629,25 @@ cudaError_t launch_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx,
                                int rows, int D, void* dx, int lddx, float* dw, float* ws, cudaStream_t s,
                                unsigned long long* launches) {
     const NormPlan p = norm_plan(D / 8, 3, rows, rows);
-    float* sums = !dw ? nullptr : p.parts == 1 ? dw : ws;
+    // the sum in the same launch, as in launch_layernorm_bwd (2048 x 4096 rows 14.1
+    // us, against 16.1); not in place, where dx takes the place of what the slabs read
+    const int slabs = (D + 63) / 64;
+    const bool fused = dw && p.parts > 1 && p.warps == 8 && rows <= 2048 && slabs <= 128 && dx != dy && dx != x;
+    const int parts = fused && p.parts > 2 * kGb300Sms - slabs ? 2 * kGb300Sms - slabs : p.parts;
+    float* sums = !dw || fused ? nullptr : p.parts == 1 ? dw : ws;
     const int r = p.warps / p.w;
     const int v8 = (D / 8 + 32 * p.w - 1) / (32 * p.w), pieces = v8 <= 1 && p.w == 1 ? 1 : 3;
     const size_t ring = static_cast<size_t>(ring_rows(p.warps)) * 2 * pieces * 32 * p.warps * sizeof(uint4);
     const size_t end = sums && r > 1 ? static_cast<size_t>(r) * D * sizeof(float) : 0;
     const size_t smem = ring > end ? ring : end;
-    const unsigned g = static_cast<unsigned>(p.parts);
+    const ColumnWork cw = {parts, slabs, dw, nullptr, 0};
+    const unsigned g = static_cast<unsigned>(parts + (fused ? slabs : 0));
     const __nv_bfloat16 *d = static_cast<const __nv_bfloat16*>(dy), *xb = static_cast<const __nv_bfloat16*>(x),
                         *wb = static_cast<const __nv_bfloat16*>(w);
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(dx);
     cudaError_t e = cudaErrorInvalidValue;
 #define DLO_RMB(V, W, N) \
-    e = launch_big<rmsnorm_bwd_kernel<V, W, N>>(g, 32 * N, smem, s, d, lddy, xb, ldx, wb, rstd, rows, D, p.parts, o, lddx, sums)
+    e = launch_big<rmsnorm_bwd_kernel<V, W, N>>(g, 32 * N, smem, s, d, lddy, xb, ldx, wb, rstd, rows, D, parts, o, lddx, sums, cw)
     // three 8-column pieces a thread: with the next row's in registers too, five
     // would spill (8192 x 5120 rows: 89 us, 54 us with three)
     if (p.w == 1) {

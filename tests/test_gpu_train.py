@@ -353,7 +353,7 @@ def _ln_reference(x, dy, gain, add, dres, rpb):
 
 @pytest.mark.parametrize("form", ["mod", "affine", "plain"])
 @pytest.mark.parametrize("rows,D,rpb", [(1, 4, 1), (3, 64, 2), (7, 132, 7), (300, 1152, 150), (260, 1284, 100), (97, 2564, 50),
-                                        (2048, 1152, 1024), (333, 5120, 333), (20, 10244, 9), (5, 20480, 2), (700, 256, 1),
+                                        (2048, 1152, 1024), (4096, 1152, 1024), (333, 5120, 333), (20, 10244, 9), (5, 20480, 2), (700, 256, 1),
                                         (5000, 68, 1700)])
 def test_layernorm_forward_and_backward(form, rows, D, rpb):
     g = torch.Generator(device="cuda").manual_seed(rows + D)
@@ -411,7 +411,7 @@ def test_layernorm_forward_and_backward(form, rows, D, rpb):
     within(dx, r["dx"] - dres.double(), r["dx_b"], "dx without dres")
 
 
-@pytest.mark.parametrize("rows,D,pad", [(1, 8, 0), (5, 64, 16), (300, 1152, 2304), (8192 + 3, 256, 0), (77, 1288, 8), (130, 2568, 0),
+@pytest.mark.parametrize("rows,D,pad", [(1, 8, 0), (5, 64, 16), (300, 1152, 2304), (8192 + 3, 256, 0), (1900, 4104, 0), (77, 1288, 8), (130, 2568, 0),
                                         (300, 5120, 10240), (33, 7000, 0), (9, 20480, 8)])
 def test_rmsnorm_forward_and_backward(rows, D, pad):
     g = torch.Generator(device="cuda").manual_seed(rows + D)
@@ -442,8 +442,12 @@ def test_rmsnorm_forward_and_backward(rows, D, pad):
     within(dx, want, bound, "dx")
     within(dw, (DY * xh).sum(0), NORM_F * (DY * xh).abs().sum(0) + 1e-30, "dw")
     assert (whole[:, :pad] == 2.5).all()
-    keep = dx.clone()
-    backward(dy, dy, None)                           # in place
+    keep, same = dx.clone(), torch.full((D,), NAN, device="cuda")
+    inplace = dy.clone()[:, :D] if not pad else torch.cat([torch.zeros_like(whole[:, :pad]), dy], 1)[:, pad:]
+    backward(inplace, inplace, same)                 # in place, and the weight's gradient all the same
+    assert torch.equal(inplace, keep)
+    within(same, (DY * xh).sum(0), NORM_F * (DY * xh).abs().sum(0) + 1e-30, "dw in place")
+    backward(dy, dy, None)
     assert torch.equal(dy, keep)
 
 
