@@ -93,9 +93,10 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane, int
     fence_proxy_async_smem();
 }
 
-// Valid rows of sequence b: lens[b] taken into 0 .. n, or n.
+// Valid rows of sequence b: lens[b] taken into 0 .. n, or n.  Read from L2: a kernel
+// may do so before its programmatic-launch wait.
 __device__ __forceinline__ int seq_len(const int* lens, int b, int n) {
-    return lens ? min(max(lens[b], 0), n) : n;
+    return lens ? min(max(__ldcg(lens + b), 0), n) : n;
 }
 
 // One past the last key that query i sees (off = nk - nq, cb = causal block,

@@ -640,7 +640,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int key0 = kt * kTile, off = g.nk - g.nq;
     const int qtiles = (g.nq + kTile - 1) / kTile;
 
-    pdl_wait();
+    // This grid starts while dq_kernel, whose every CTA has waited for what came
+    // before, ends: all inputs are there, and only the row statistics, dq_kernel's
+    // own, need the wait.  Every CTA waits before it ends, so that whoever waits
+    // for this grid has waited for dq_kernel too.  (In a graph, 256 tokens of 4 heads
+    // of 64: 10.1 us for the two launches, 11.3 with the wait here; 2 x 16 heads of
+    // 72, 1024 tokens: 48.8, 50.4 with it.)
     const int qlen = seq_len(g.q_lens, b, g.nq), klen = seq_len(g.k_lens, b, g.nk);
     // query tiles [t0, t1) of each of the group's heads, one after the other
     const int t0 = max(0, query_begin(key0, off, g.causal_block)) / kTile;
@@ -654,6 +659,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const size_t part_at = ((static_cast<size_t>(split) * gridDim.z + b) * g.nk + key0) * ldp + hk * g.hd;
     const bool parts = g.splits_k > 1;
     if (n <= 0) {
+        pdl_wait();
         if (parts) {
             zero_out(g.part_k + part_at, ldp, min(kTile, g.nk - key0), g.hd);
             zero_out(g.part_v + part_at, ldp, min(kTile, g.nk - key0), g.hd);
@@ -717,6 +723,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 if (ok) {
                     mbar_arrive_expect_tx(full0, P::TILE + kStatBytes);
                     load_tile<NB, TAIL>(sb + P::R_OFF + q.s * P::TILE, &maps.q, &maps.qt, h, qt * kTile, b, full0);
+                    if (i == 0) pdl_wait();
                     bulk_load(sb + P::STAT_OFF + i % P::STATS * kStatBytes,
                               g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16), kStatBytes, full0);
                     if (!raw) in.add(q);

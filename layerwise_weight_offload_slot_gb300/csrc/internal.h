@@ -15,7 +15,7 @@ namespace dlo {
 bool pdl_enabled();
 
 // Launch `kernel` on `s` allowing programmatic stream serialisation (the
-// kernel must run pdl_wait() before touching global memory).
+// kernel runs pdl_wait() as ptx.cuh says).
 template <typename... KArgs, typename... Args>
 cudaError_t launch_k(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                      Args&&... args) {

@@ -22,13 +22,16 @@ __device__ __forceinline__ unsigned long long global_timer_ns() {
 }
 
 // ------------------------------------------------------------------ programmatic dependent launch
-// Every kernel of this library runs pdl_wait() before its first global memory
-// access (read or write), so a kernel launched with programmatic stream
-// serialisation may be scheduled -- and run its set-up -- while its
-// predecessor on the stream finishes; pdl_wait returns once every
+// Every kernel of this library runs pdl_wait() before its first access to global
+// memory (read or write) that a kernel still running may touch, so a kernel
+// launched with programmatic stream serialisation may be scheduled -- and run
+// its set-up -- while its predecessor on the stream finishes; pdl_wait returns once every
 // prerequisite grid has completed and its memory is visible (immediately when
 // there is none).  pdl_launch_dependents lets the next kernel be scheduled as
 // soon as every CTA of this grid has issued it or exited.
+// What a kernel reads before pdl_wait() was written before its predecessor began:
+// weights, or (dkv_kernel) inputs that the predecessor itself waited for before it let
+// this grid start.  Such reads go around L1 (TMA, ld.cg).
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch_dependents() {

@@ -576,3 +576,45 @@ def test_attention_keeps_its_bits_over_many_calls(case):
             for a, b in zip(keep, (p.o, p.lse, *grads)):
                 differ += (a != b).sum()
     assert int(differ.item()) == 0 and int(p.err.item()) == 0
+
+
+@pytest.mark.parametrize("case", [(1, 4, 4, 64, 256, 256), (2, 8, 8, 128, 300, 77), (2, 16, 16, 72, 1024, 1024), (2, 16, 4, 64, 40, 1500)],
+                         ids=lambda c: "x".join(map(str, c)))
+@pytest.mark.parametrize("graph", [False, True], ids=["eager", "graph"])
+def test_attention_backward_reads_what_was_written_just_before(case, graph):
+    """Inputs and lengths change in place right before each call, nothing waits on the host:
+    every launch of the call has to see the new ones, whichever starts early."""
+    nq, nk = case[4:6]
+    lens = [None] * 3 if case[0] == 1 else [([nq, nq - 19], [nk - 5, nk]), ([nq - 33, nq], [nk, nk - 40]), ([nq - 1, 1], [1, nk - 1])]
+    sets = [Problem(*case, 0, *(lens[i] or (None, None)), seed=50 + i, fused=False) for i in range(3)]
+    want = []
+    for s in sets:
+        s.forward()
+        want.append(s.grads())
+        torch.cuda.synchronize()
+        s.backward(want[-1])
+        torch.cuda.synchronize()
+    names = ("q", "k", "v", "do", "o", "lse") + (() if lens[0] is None else ("q_lens", "k_lens"))
+    p = Problem(*case, 0, *(lens[0] or (None, None)), seed=50, fused=False)
+    grads = p.grads()
+    ws = bytes_(dlo.dlo_attention_bwd_workspace_bytes(p.desc(grads)))
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+
+    def one_round():
+        for s, w in zip(sets, want):
+            for n in names:
+                getattr(p, n).copy_(getattr(s, n))
+            p.backward(grads, ws)
+            for a, b in zip(grads, w):
+                differ.add_((a != b).sum())
+
+    one_round()
+    torch.cuda.synchronize()
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            one_round()
+        one_round = g.replay
+    for _ in range(30):
+        one_round()
+    assert int(differ.item()) == 0 and int(p.err.item()) == 0
