@@ -618,3 +618,35 @@ def test_attention_backward_reads_what_was_written_just_before(case, graph):
     for _ in range(30):
         one_round()
     assert int(differ.item()) == 0 and int(p.err.item()) == 0
+
+
+@pytest.mark.parametrize("nq,nk,cb,klen", [(40, 2, 0, None), (130, 300, 0, 3), (64, 64, 1, None), (257, 128, 0, 100), (100, 100, 10, 77)])
+@pytest.mark.parametrize("hd", [64, 128])
+def test_attention_gradients_of_few_keys_do_not_carry_the_rounding_of_o(nq, nk, cb, klen, hd):
+    """Rows that lie in one key tile: D is the sum of P dP, off by what fp32 makes of P (f, relative)
+    and dP (2^-20 of |do||v|), so dS is right to f |dS| + P (f + 2^-20) (|do||v| + sum P |do||v|)
+    before its rounding.  With D from a bf16 O, dQ misses this bound."""
+    H = 3
+    p = Problem(1, H, H, hd, nq, nk, cb, None, None if klen is None else [klen], seed=77, fused=False)
+    p.forward()
+    grads = p.grads()
+    p.backward(grads)
+    torch.cuda.synchronize()
+    assert int(p.err.item()) == 0
+    n = nk if klen is None else klen
+    ref = p.reference()
+    i = torch.arange(nq, device="cuda")[:, None] + nk - nq
+    j = torch.arange(n, device="cuda")[None]
+    see = torch.ones(nq, n, dtype=torch.bool, device="cuda")
+    if cb:
+        see = (i >= 0) & (torch.div(i, cb, rounding_mode="floor") >= torch.div(j, cb, rounding_mode="floor"))
+    for h in range(H):
+        at = slice(h * hd, (h + 1) * hd)
+        q, k, v, do = (t.double() for t in (p.q[0, :, at], p.k[0, :n, at], p.v[0, :n, at], p.do[0, :, at]))
+        pr = torch.nan_to_num(torch.softmax((q @ k.T / math.sqrt(hd)).masked_fill(~see, -math.inf), 1))
+        dp, m = do @ v.T, do.abs() @ v.abs().T
+        ds = pr * (dp - (pr * dp).sum(1, keepdim=True))
+        ds_b = (U + F) * ds.abs() + pr * (F + 2.0 ** -20) * (m + (pr * m).sum(1, keepdim=True))
+        for name, got, b in (("dq", grads[0][0, :, at], ds_b @ k.abs()), ("dk", grads[1][0, :n, at], ds_b.T @ q.abs())):
+            want = ref[name][0, :got.shape[0], h]
+            within(got, want, b / math.sqrt(hd) + U * want.abs() + 1e-30, name)
