@@ -15,7 +15,7 @@
 // fixed order, so results do not depend on the schedule.  Few rows take one
 // launch instead: more CTAs of it read dy and x again for the column sums.
 // Sums and statistics are fp32.  (32760 x 5120 LayerNorm backward: 384 us, 6.1
-// TB/s; 8192 x 5120 RMSNorm forward 27.9 us, 6.0 TB/s, backward 49 us.)
+// TB/s; 8192 x 5120 RMSNorm forward 27.9 us, 6.0 TB/s, backward 48 us.)
 #include <cuda_bf16.h>
 
 #include "internal.h"
