@@ -598,6 +598,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             if (j > 0) {
                 const Slot k = first(j - 1);
                 if (!warp_wait(m.empty + 8 * k.s, k.ph, abort_flag)) { ok = false; break; }
+                tc_fence_after();       // the store stays behind dQ_{j-1}'s reads
             }
             tmem_st_32x32b_x16(tl + 256 + kCols / 2 * e, w);
             tmem_wait_st();
@@ -950,6 +951,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 // the last reader of its columns, dV_{i-1}, releases its dO slot when done
                 const Slot t = second(i - 1);
                 if (i > 0 && !warp_wait(m.empty + 8 * t.s, t.ph, abort_flag)) { ok = false; break; }
+                tc_fence_after();
                 tmem_st_32x32b_x16(tl + M::P_COL + kCols / 2 * e, w);
             } else {
                 tmem_st_32x32b_x16(ts, w);
@@ -982,6 +984,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 // the last reader of its columns, dK_{i-1}, releases its Q slot when done
                 const Slot t = first(i - 1);
                 if (i > 0 && !warp_wait(m.empty + 8 * t.s, t.ph, abort_flag)) { ok = false; break; }
+                tc_fence_after();
                 tmem_st_32x32b_x16(tl + M::DS_COL + kCols / 2 * e, w);
             } else {
                 tmem_st_32x32b_x16(ts + 128, w);
