@@ -435,7 +435,10 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             if (lane == 0) fail();
         } else {
             tc_fence_after();
-            const float inv = TR && l == 0.f ? 0.f : 1.f / l;
+            // TR: l = 0 where the row sees no key; its accumulator is 0 too, or NaN
+            // where the other rows' keys hold an infinite V
+            const bool none = TR && l == 0.f;
+            const float inv = none ? 0.f : 1.f / l;
             const int grow = qt * tq + (TR ? row >> tr.lg : row);
             const int h0 = h;
             if constexpr (TR) h += row & ((1 << tr.lg) - 1);
@@ -463,7 +466,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
                         uint32_t w[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            w[i] = pack_bf16x2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
+                            w[i] = none ? 0 : pack_bf16x2(__uint_as_float(r[2 * i]) * inv, __uint_as_float(r[2 * i + 1]) * inv);
                         put_row<NB, TAIL>(smem + P::Q_OFF, row, c, w);
                         continue;
                     }
