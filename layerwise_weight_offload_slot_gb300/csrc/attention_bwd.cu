@@ -242,15 +242,20 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi_mid, uint32_t& lo) 
 // One thread's part of an accumulator row (32-column chunks first, first +
 // step, ...) times `scale`: in fp32 to `part` if that is set, else in bf16 to the
 // tile in shared memory that TMA then stores (rows and columns past the tensor
-// are not written).
+// are not written).  `none`: zeros instead, for a row without a visible pair; its
+// accumulator is 0, or NaN where the tile's other rows met an infinity.
 template <int NB, bool TAIL>
-__device__ __forceinline__ void store_row(uint32_t t, uint8_t* tile, int row, float* part, int hd, bool live, float scale, int first,
-                                          int step) {
+__device__ __forceinline__ void store_row(uint32_t t, uint8_t* tile, int row, float* part, int hd, bool live, bool none, float scale,
+                                          int first, int step) {
 #pragma unroll 1
     for (int c = first; c < (AttnTile<NB, TAIL>::HDP + 31) / 32; c += step) {
         uint32_t r[32], w[16];
         tmem_ld_32x32b_x32(t + c * 32, r);
         tmem_wait_ld_r(r);
+        if (none) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) r[k] = 0;
+        }
         if (part) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -613,7 +618,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             tc_fence_after();
             // the slots' tiles have all been read: the first one takes the result
             store_row<NB, TAIL>(tl + 384, smem + P::R_OFF, row, part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < g.nq,
-                                g.scale, e, kGroups);
+                                end <= 0, g.scale, e, kGroups);
             if (!part0) {
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -1003,7 +1008,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             const bool k = e & 1;
             float* part = parts ? (k ? g.part_k : g.part_v) + part_at + static_cast<size_t>(row) * ldp : nullptr;
             store_row<NB, TAIL>(tl + (k ? M::DK_COL : M::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < g.nk,
-                                k ? g.scale : 1.f, e >> 1, kGroups / 2);
+                                begin >= qlen, k ? g.scale : 1.f, e >> 1, kGroups / 2);
             if (!parts) {
                 fence_proxy_async_smem();
                 __syncwarp();

@@ -62,3 +62,16 @@ def test_forward_rows_that_see_nothing_are_zero_beside_infinities(case):
     assert int(p.err.item()) == 0
     assert (p.o[q_out] == 0).all(), "O"
     assert (p.lse.transpose(1, 2)[q_out] == -math.inf).all(), "lse"
+
+
+@pytest.mark.parametrize("case", CASES, ids=IDS)
+def test_gradients_of_rows_without_a_part_are_zero_beside_infinities(case):
+    p, q_out, k_out = infinities(case)
+    p.forward()
+    grads = p.grads()
+    p.backward(grads)
+    torch.cuda.synchronize()
+    assert int(p.err.item()) == 0
+    assert (grads[0][q_out] == 0).all(), "dQ"
+    assert (grads[1][k_out] == 0).all(), "dK"
+    assert (grads[2][k_out] == 0).all(), "dV"
