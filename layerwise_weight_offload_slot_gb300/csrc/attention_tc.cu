@@ -677,7 +677,7 @@ cudaError_t launch_attention_fwd(const dlo_attn& a, const void* Q, const void* K
                     plan.splits, plan.lg, static_cast<float*>(ws), nullptr};
     tr.pl = tr.po + tr.splits * rows * a.head_dim;
     const int hd = a.head_dim;
-    const bool duo = plan.ctas > kGb300Sms;      // as for launch_attention_tc
+    const bool duo = attn_duo_enabled() && plan.ctas > kGb300Sms;      // as for launch_attention_tc
     cudaError_t e;
 #define DLO_AF(NB, TAIL, DUO)                                                                                         e = run_tc<NB, TAIL, DUO, true>(Q, K, V, O, a.batch, a.heads, hd, a.nq, a.nk, a.ldq, a.ldk, a.ldv, a.ldo, err,                                     s, launches, tr)
     if (hd <= 64) {
