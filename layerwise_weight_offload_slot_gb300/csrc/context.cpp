@@ -1499,10 +1499,6 @@ extern "C" dlo_status dlo_verify_slot(dlo_ctx* c, int slot, int block) {
 
 // ===================================================================== unit ops
 
-namespace {
-unsigned long long g_op_launches = 0;
-}  // namespace
-
 namespace dlo {
 
 dlo_status op_fail(dlo_status st, const std::string& msg) {
@@ -1524,7 +1520,7 @@ dlo_status op_inval(const char* m) { return op_fail(DLO_EINVAL, m); }
 
 extern "C" dlo_status dlo_op_wait_selftest(int* err, void* stream) {
     if (!err || !aligned(err, 4)) return op_inval("err must be a 4-byte aligned device int");
-    return op_result(launch_wait_selftest(err, static_cast<cudaStream_t>(stream), &g_op_launches));
+    return op_result(launch_wait_selftest(err, static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
 extern "C" dlo_status dlo_debug_device_timeout(dlo_ctx* c) {
@@ -1544,7 +1540,7 @@ extern "C" dlo_status dlo_op_quantize_act(const void* x, int rows, int cols, int
     if (!aligned(x, 16) || !aligned(q, 16) || !aligned(scale, 4) || !aligned(scratch, 4))
         return op_inval("x and q must be 16-byte aligned");
     return op_result(launch_quantize_e4m3(x, rows, cols, ld, q, scale, scratch, static_cast<cudaStream_t>(stream),
-                                          &g_op_launches));
+                                          Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_gemm_w8a8(const void* A, const float* a_scale, const void* W, const float* scales,
@@ -1611,7 +1607,7 @@ dlo_status op_gemm_params(const void* A, const void* W, int w_dtype, const float
 }
 
 dlo_status op_launch_gemm(const GemmParams& p, cudaStream_t s) {
-    return op_result(launch_gemm(p, s, &g_op_launches));
+    return op_result(launch_gemm(p, s, Uncounted()));
 }
 
 }  // namespace dlo
@@ -1625,7 +1621,7 @@ extern "C" dlo_status dlo_op_attention(const void* Q, const void* K, const void*
     if (ldq % 8 || ldk % 8 || ldv % 8 || ldo % 8) return op_inval("ld % 8 != 0");
     if (!aligned(Q, 16) || !aligned(K, 16) || !aligned(V, 16) || !aligned(O, 16)) return op_inval("alignment");
     return op_result(launch_attention(Q, K, V, O, batch, heads, head_dim, nq, nk, ldq, ldk, ldv, ldo,
-                                      nullptr, static_cast<cudaStream_t>(stream), &g_op_launches));
+                                      nullptr, static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_layernorm(const float* x, int rows, int D, int rows_per_batch,
@@ -1635,25 +1631,25 @@ extern "C" dlo_status dlo_op_layernorm(const float* x, int rows, int D, int rows
     if ((shift == nullptr) != (scale == nullptr) || (w == nullptr) != (b == nullptr)) return op_inval("pairs");
     if (scale && (mod_ld % 4 || !aligned(scale, 16) || !aligned(shift, 16))) return op_inval("mod layout");
     return op_result(launch_layernorm(x, rows, D, rows_per_batch, shift, scale, mod_ld, w, b, eps, out,
-                                      static_cast<cudaStream_t>(stream), &g_op_launches));
+                                      static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_rmsnorm(void* x, int rows, int D, int ld, int col0, const void* w, float eps,
                                      void* stream) {
     if (!x || !w || rows < 1 || D < 8 || D % 8 || ld % 8 || col0 % 8 || col0 + D > ld) return op_inval("rmsnorm args");
-    return op_result(launch_rmsnorm(x, rows, D, ld, col0, w, eps, static_cast<cudaStream_t>(stream), &g_op_launches));
+    return op_result(launch_rmsnorm(x, rows, D, ld, col0, w, eps, static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_adaln(const void* cvec, int B, int C, const void* W, const void* bias, int N,
                                    float* m, void* stream) {
     if (!cvec || !W || !bias || !m || B < 1 || C < 8 || C % 8 || N < 1) return op_inval("adaln args");
-    return op_result(launch_adaln(cvec, B, C, W, bias, N, m, static_cast<cudaStream_t>(stream), &g_op_launches));
+    return op_result(launch_adaln(cvec, B, C, W, bias, N, m, static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_stage(void* dst, const void* src, size_t bytes, int mode, void* stream) {
     if (!dst || !src || bytes % 16 || !aligned(dst, 16) || !aligned(src, 16)) return op_inval("stage args");
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (mode == DLO_STAGE_GATHER) return op_result(launch_gather(dst, src, bytes, s, &g_op_launches));
+    if (mode == DLO_STAGE_GATHER) return op_result(launch_gather(dst, src, bytes, s, Uncounted()));
     if (mode == DLO_STAGE_MEMCPY) return op_result(cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDefault, s));
     return op_inval("mode");
 }

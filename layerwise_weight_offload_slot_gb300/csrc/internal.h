@@ -53,6 +53,13 @@ cudaError_t launch_big(dim3 grid, dim3 block, size_t smem, cudaStream_t s, Args&
     return launch_k(Kernel, grid, block, smem, s, static_cast<Args&&>(args)...);
 }
 
+// A launcher's `launches` for the dlo_op_* calls, which keep no statistics: each
+// call's own, since they may run in several threads at once.
+struct Uncounted {
+    unsigned long long n = 0;
+    operator unsigned long long*() && { return &n; }
+};
+
 // ------------------------------------------------------------------ layout
 
 // Linear weights stored as E4M3 codes (W8A16 or W8A8).

@@ -5,8 +5,6 @@ using namespace dlo;
 
 namespace {
 
-unsigned long long g_train_launches = 0;
-
 constexpr int kMaxRows = 1 << 30;
 constexpr int kMaxNormDim = 20480;
 
@@ -53,7 +51,7 @@ extern "C" dlo_status dlo_op_attention_fwd(const dlo_attn* a, const void* Q, con
     if (ws_bytes < need) return op_fail(DLO_ENOMEM, "workspace too small");
     if (need && (!ws || !aligned_to(ws, 256))) return inval("workspace must be 256-byte aligned");
     return op_result(launch_attention_fwd(*a, Q, K, V, O, lse, ws, err, static_cast<cudaStream_t>(stream),
-                                          &g_train_launches));
+                                          Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_attention_bwd(const dlo_attn* a, const void* Q, const void* K, const void* V,
@@ -73,7 +71,7 @@ extern "C" dlo_status dlo_op_attention_bwd(const dlo_attn* a, const void* Q, con
     if (ws_bytes < attention_bwd_workspace(*a)) return op_fail(DLO_ENOMEM, "workspace too small");
     if (!ws || !aligned_to(ws, 256)) return inval("workspace must be 256-byte aligned");
     return op_result(launch_attention_bwd(*a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, err,
-                                          static_cast<cudaStream_t>(stream), &g_train_launches));
+                                          static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_layernorm_fwd(const float* x, int rows, int D, int rows_per_batch, const float* shift,
@@ -89,7 +87,7 @@ extern "C" dlo_status dlo_op_layernorm_fwd(const float* x, int rows, int D, int 
         !aligned_to(rstd, 4))
         return inval("alignment");
     return op_result(launch_layernorm(x, rows, D, rows_per_batch, shift, scale, mod_ld, w, b, eps, out,
-                                      static_cast<cudaStream_t>(stream), &g_train_launches, mean, rstd));
+                                      static_cast<cudaStream_t>(stream), Uncounted(), mean, rstd));
 }
 
 extern "C" size_t dlo_layernorm_bwd_workspace_bytes(int rows, int D, int rows_per_batch) {
@@ -118,7 +116,7 @@ extern "C" dlo_status dlo_op_layernorm_bwd(const void* dy, const float* x, const
     }
     return op_result(launch_layernorm_bwd(dy, x, mean, rstd, rows, D, rows_per_batch, scale, mod_ld, w, dres, dx, dshift,
                                           dscale, scale ? dmod_ld : D, static_cast<float*>(ws),
-                                          static_cast<cudaStream_t>(stream), &g_train_launches));
+                                          static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
 extern "C" dlo_status dlo_op_rmsnorm_fwd(const void* x, int ldx, int rows, int D, const void* w, float eps, void* y,
@@ -130,7 +128,7 @@ extern "C" dlo_status dlo_op_rmsnorm_fwd(const void* x, int ldx, int rows, int D
     if (!(eps > 0.f)) return inval("eps must be > 0");
     if (!aligned_to(x, 16) || !aligned_to(w, 16) || !aligned_to(y, 16) || !aligned_to(rstd, 4)) return inval("alignment");
     return op_result(launch_rmsnorm_fwd(x, ldx, rows, D, w, eps, y, ldy, rstd, static_cast<cudaStream_t>(stream),
-                                        &g_train_launches));
+                                        Uncounted()));
 }
 
 extern "C" size_t dlo_rmsnorm_bwd_workspace_bytes(int rows, int D) {
@@ -154,5 +152,5 @@ extern "C" dlo_status dlo_op_rmsnorm_bwd(const void* dy, int lddy, const void* x
         if (!ws || !aligned_to(ws, 16)) return inval("workspace must be 16-byte aligned");
     }
     return op_result(launch_rmsnorm_bwd(dy, lddy, x, ldx, w, rstd, rows, D, dx, lddx, dw, static_cast<float*>(ws),
-                                        static_cast<cudaStream_t>(stream), &g_train_launches));
+                                        static_cast<cudaStream_t>(stream), Uncounted()));
 }
