@@ -573,7 +573,8 @@ dlo_status dlo_op_stage(void* dst, const void* src, size_t bytes, int mode, void
  * used, whatever it holds.
  * batch, heads, kv_heads, nq, nk >= 1; batch <= 65535; heads <= 65535;
  * heads % kv_heads == 0; head_dim % 8 == 0 and <= 128; ld* % 8 == 0 and at
- * least the row they stride; bf16 pointers 16-byte aligned. */
+ * least the row they stride; bf16 pointers 16-byte, fp32 and int32 ones
+ * 4-byte aligned. */
 typedef struct dlo_attn {
     int batch, heads, kv_heads, head_dim, nq, nk;
     int causal_block;                 /* 0: every key                          */

@@ -24,6 +24,11 @@ const char* attn_problem(const dlo_attn* a) {
     return nullptr;
 }
 
+// The int32 operands, read where a kernel starts.
+bool bad_words(const dlo_attn* a, const int* err) {
+    return !aligned_to(a->q_lens, 4) || !aligned_to(a->k_lens, 4) || !aligned_to(err, 4);
+}
+
 bool bad_ld(int ld, int heads, int head_dim) { return ld % 8 || ld < heads * head_dim; }
 
 }  // namespace
@@ -45,7 +50,8 @@ extern "C" dlo_status dlo_op_attention_fwd(const dlo_attn* a, const void* Q, con
     if (bad_ld(a->ldq, a->heads, a->head_dim) || bad_ld(a->ldk, a->kv_heads, a->head_dim) ||
         bad_ld(a->ldv, a->kv_heads, a->head_dim) || bad_ld(a->ldo, a->heads, a->head_dim))
         return inval("ld % 8 != 0 or smaller than its row");
-    if (!aligned_to(Q, 16) || !aligned_to(K, 16) || !aligned_to(V, 16) || !aligned_to(O, 16) || !aligned_to(lse, 4))
+    if (!aligned_to(Q, 16) || !aligned_to(K, 16) || !aligned_to(V, 16) || !aligned_to(O, 16) || !aligned_to(lse, 4) ||
+        bad_words(a, err))
         return inval("alignment");
     const size_t need = attention_fwd_workspace(*a);
     if (ws_bytes < need) return op_fail(DLO_ENOMEM, "workspace too small");
@@ -67,7 +73,7 @@ extern "C" dlo_status dlo_op_attention_bwd(const dlo_attn* a, const void* Q, con
     for (const void* p : {Q, K, V, O, dO, static_cast<const void*>(dQ), static_cast<const void*>(dK),
                           static_cast<const void*>(dV)})
         if (!aligned_to(p, 16)) return inval("alignment");
-    if (!aligned_to(lse, 4)) return inval("alignment");
+    if (!aligned_to(lse, 4) || bad_words(a, err)) return inval("alignment");
     if (ws_bytes < attention_bwd_workspace(*a)) return op_fail(DLO_ENOMEM, "workspace too small");
     if (!ws || !aligned_to(ws, 256)) return inval("workspace must be 256-byte aligned");
     return op_result(launch_attention_bwd(*a, Q, K, V, O, lse, dO, dQ, dK, dV, ws, err,
