@@ -634,7 +634,9 @@ dlo_status dlo_op_rmsnorm_fwd(const void* x, int ldx, int rows, int D, const voi
                               int ldy, float* rstd, void* stream);
 
 /* Gradients of dlo_op_rmsnorm_fwd: dx bf16 rows of stride lddx (may be dy or x
- * themselves, with the same stride), dw fp32 [D] or NULL. */
+ * themselves, with the same stride), dw fp32 [D] or NULL.  dw is summed in one
+ * order in place and in another out of place: each gives the same bits every
+ * time, the two may differ in the last ones. */
 size_t dlo_rmsnorm_bwd_workspace_bytes(int rows, int D);
 dlo_status dlo_op_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx, const void* w,
                               const float* rstd, int rows, int D, void* dx, int lddx, float* dw, void* ws,

@@ -26,7 +26,7 @@
 // What bounds it (measured on copies with parts left out, head dim 128): the
 // elementwise work is hidden (exponentials left out: same time), loads alone
 // take 0.77 us a tile of the dQ kernel, the products 1.2 us where their
-// instructions need 0.8 at 1.9 GHz; the tensor core is 53% (dQ) and 70% (dK, dV)
+// instructions need 0.8 at 1.9 GHz; the tensor core is 56% (dQ) and 70% (dK, dV)
 // active over a whole launch, the rest is the start and end of each CTA (~6 us,
 // one CTA per SM) and waits between products.  Issue matters: from a branch of a
 // single thread an MMA takes ~48 cycles to issue, from a converged warp with

@@ -10,10 +10,15 @@
 // Everything is bound by HBM: each element of x, dy (and dres) is read once and
 // dx written once.  A row lives in the registers of W warps, which also hold
 // the gain of their columns (a CTA stays within one batch) and the two
-// running column sums of every row they have seen; the sums of a CTA leave it
+// running column sums of every row they have seen (above 10240 columns, LayerNorm,
+// or 12288, RMSNorm, 32 warps share a row with 64 registers a thread, and 664 or 350
+// bytes a thread spill: 2048 x 16384, whose column sums take a second launch, runs at
+// 1.9 and 1.5 TB/s); the sums of a CTA leave it
 // once, as one partial row, and a second launch adds the partial rows in a
 // fixed order, so results do not depend on the schedule.  Few rows take one
-// launch instead: more CTAs of it read dy and x again for the column sums.
+// launch instead: more CTAs of it read dy and x again for the column sums (their
+// order is another one, and RMSNorm in place cannot take it, so the last bits of
+// its dw differ between in place and not).
 // Sums and statistics are fp32.  (32760 x 5120 LayerNorm backward: 384 us, 6.1
 // TB/s; 8192 x 5120 RMSNorm forward 27.9 us, 6.0 TB/s, backward 48 us.)
 #include <cuda_bf16.h>
