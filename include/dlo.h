@@ -642,6 +642,103 @@ dlo_status dlo_op_rmsnorm_bwd(const void* dy, int lddy, const void* x, int ldx, 
                               const float* rstd, int rows, int D, void* dx, int lddx, float* dw, void* ws,
                               size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- packed batches
+ * Sequences of different lengths in one buffer, without padding: sequence b is
+ * rows starts[b] .. starts[b + 1] - 1 of its matrix (device int32 [batch + 1],
+ * not decreasing; each is taken into 0 .. rows).  Rows before the first and
+ * behind the last sequence are never used and stay as they are in every
+ * output.  The lengths are read on the device: a captured call follows
+ * them where they change in place.  Called as the training ops; the same
+ * rules hold for streams, workspaces, captures, overlap and the order of sums. */
+
+/* Row starts and positions of a packed batch from the sequences' extents.
+ * grids int32 [batch, axes]: the extents of each sequence, e.g. (frames, rows,
+ * columns) of a clip or (tokens) of a prompt; its length is their product
+ * (an extent below 0 counts as 0).  starts[b] = min(rows, the lengths before
+ * b), so sequences that do not fit into `rows` are cut.  positions (int32
+ * [rows, axes] or NULL): row starts[b] + i has offsets[b, a] (int32 [batch,
+ * axes] or NULL: 0) plus its place in the grid, the last axis fastest.
+ * 1 <= batch <= 65535, 1 <= axes <= 4, 1 <= rows <= 2^30; 4-byte alignment. */
+dlo_status dlo_op_packed_plan(const int* grids, const int* offsets, int batch, int axes, int rows, int* starts,
+                              int* positions, void* stream);
+
+/* Rotary positions.  A head's first columns are split among the axes, axis[a].dim
+ * of them to axis a; pair p of an axis turns by position * f_p, f_p =
+ * theta^(-2 p / dim), and the columns behind stay as they are.  With all pairs of
+ * a head counted through, n in number, pair p is columns (2 p, 2 p + 1)
+ * (DLO_ROPE_INTERLEAVED) or (p, p + n) (DLO_ROPE_HALF):
+ *   (u, v) -> amp * (u cos - v sin, u sin + v cos).
+ * Scaled for contexts `factor` times as long:
+ *   DLO_ROPE_LINEAR    f / factor
+ *   DLO_ROPE_BASE      theta * factor^(dim / (dim - 2)) in place of theta
+ *   DLO_ROPE_BY_TURNS  f (k + (1 - k) / factor): k rises from 0 to 1 as the turns
+ *                      f length / 2 pi in the original length go from slow to fast
+ *   DLO_ROPE_BY_INDEX  likewise with k falling from 1 to 0 over the pairs p from
+ *                      floor(p(fast)) to ceil(p(slow)), p(t) = dim ln(length /
+ *                      (2 pi t)) / (2 ln theta) the pair of t turns, taken into
+ *                      0 .. dim - 1
+ * heads <= 65535; head_dim % 8 == 0 and <= 256; dim even, >= 2, together <= head_dim;
+ * theta > 1; factor >= 1; length > 0; 0 < slow < fast. */
+#define DLO_ROPE_AXES 4
+#define DLO_ROPE_INTERLEAVED 0
+#define DLO_ROPE_HALF 1
+#define DLO_ROPE_PLAIN 0
+#define DLO_ROPE_LINEAR 1
+#define DLO_ROPE_BASE 2
+#define DLO_ROPE_BY_TURNS 3
+#define DLO_ROPE_BY_INDEX 4
+typedef struct dlo_rope_axis {
+    int dim, scaling;
+    double theta, factor, length, fast, slow;   /* those that the scaling uses  */
+} dlo_rope_axis;
+typedef struct dlo_rope {
+    int heads, head_dim, layout, axes;
+    dlo_rope_axis axis[DLO_ROPE_AXES];
+    int ldx, ldy;                     /* row strides of x (dx) and y (dy), elements */
+    float amp;
+} dlo_rope;
+
+/* The table of the two ops below: step of pair p = f_p / 2 pi as a 64-bit fraction
+ * of a turn.  Host memory; n must be the number of pairs (the dims' sum / 2).  A
+ * program lays it out once and keeps it on the device. */
+dlo_status dlo_rope_steps(const dlo_rope* r, uint64_t* steps, int n);
+
+/* y = x (bf16 [rows], `heads` heads from the pointer's column on) turned by its
+ * rows' positions (int32 [rows, axes], any value); q and k that lie side by side
+ * in fused rows are one call.  In place: y = x and ldy = ldx.  Angles are exact
+ * to 2^-32 of a turn.  ld % 8 == 0 and at least the row; x, y 16-byte, steps
+ * (device) 8-byte, positions 4-byte aligned. */
+dlo_status dlo_op_rope_fwd(const dlo_rope* r, const void* x, const int* positions, const uint64_t* steps, int rows,
+                           void* y, void* stream);
+
+/* dx = dy turned back (and times amp), rows of stride ldx from rows of stride ldy. */
+dlo_status dlo_op_rope_bwd(const dlo_rope* r, const void* dy, const int* positions, const uint64_t* steps, int rows,
+                           void* dx, void* stream);
+
+/* Attention over packed sequences: that of dlo_attn, where sequence b has the
+ * nq = q_starts[b + 1] - q_starts[b] queries and nk keys likewise (k_starts may be
+ * q_starts), the causal mask sets its last query against its last key, and row
+ * r of a matrix starts at r * ld.  lse is fp32 [heads, rows_q].  A sequence
+ * without keys has O = 0, lse = -inf, dQ = 0; one without queries dK = dV = 0.
+ * batch, heads <= 65535; 1 <= rows_q, rows_k <= 2^30, the rows of the buffers; else
+ * as dlo_attn. */
+typedef struct dlo_attn_packed {
+    int batch, heads, kv_heads, head_dim, rows_q, rows_k;
+    int causal_block;
+    int ldq, ldk, ldv, ldo;
+    int lddq, lddk, lddv, lddo;
+    const int* q_starts;
+    const int* k_starts;
+} dlo_attn_packed;
+
+size_t dlo_attention_packed_fwd_workspace_bytes(const dlo_attn_packed* a);
+size_t dlo_attention_packed_bwd_workspace_bytes(const dlo_attn_packed* a);
+dlo_status dlo_op_attention_packed_fwd(const dlo_attn_packed* a, const void* Q, const void* K, const void* V, void* O,
+                                       float* lse, void* ws, size_t ws_bytes, int* err, void* stream);
+dlo_status dlo_op_attention_packed_bwd(const dlo_attn_packed* a, const void* Q, const void* K, const void* V,
+                                       const void* O, const float* lse, const void* dO, void* dQ, void* dK, void* dV,
+                                       void* ws, size_t ws_bytes, int* err, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

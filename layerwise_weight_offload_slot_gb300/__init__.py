@@ -32,6 +32,9 @@ STAGE_MEMCPY, STAGE_GATHER, STAGE_PER_TENSOR = 0, 1, 2
 HOST_PINNED, HOST_REGISTER, HOST_PAGEABLE = 1, 2, 4
 DT_BF16, DT_E4M3, DT_F32, DT_U8 = 0, 1, 2, 3
 EPI_BIAS, EPI_GELU, EPI_RESIDUAL = 0, 1, 2
+ROPE_AXES = 4
+ROPE_INTERLEAVED, ROPE_HALF = 0, 1
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_BY_TURNS, ROPE_BY_INDEX = 0, 1, 2, 3, 4
 
 STATUS_NAMES = {0: "OK", -1: "EINVAL", -2: "ESTATE", -3: "ENOMEM", -4: "ECUDA",
                 -5: "EREGISTER", -6: "ETIMEDOUT", -7: "EUNSUPPORTED", -8: "EMISMATCH"}
@@ -87,6 +90,23 @@ class dlo_attn(ctypes.Structure):
                 ("batch", "heads", "kv_heads", "head_dim", "nq", "nk", "causal_block", "ldq", "ldk", "ldv",
                  "ldo", "lddq", "lddk", "lddv", "lddo")] + [("q_lens", ctypes.c_void_p),
                                                             ("k_lens", ctypes.c_void_p)]
+
+
+class dlo_rope_axis(ctypes.Structure):
+    _fields_ = [("dim", ctypes.c_int), ("scaling", ctypes.c_int)] + [(n, ctypes.c_double) for n in
+                                                                    ("theta", "factor", "length", "fast", "slow")]
+
+
+class dlo_rope(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("heads", "head_dim", "layout", "axes")] + \
+        [("axis", dlo_rope_axis * ROPE_AXES), ("ldx", ctypes.c_int), ("ldy", ctypes.c_int), ("amp", ctypes.c_float)]
+
+
+class dlo_attn_packed(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in
+                ("batch", "heads", "kv_heads", "head_dim", "rows_q", "rows_k", "causal_block", "ldq", "ldk", "ldv",
+                 "ldo", "lddq", "lddk", "lddv", "lddo")] + [("q_starts", ctypes.c_void_p),
+                                                            ("k_starts", ctypes.c_void_p)]
 
 
 KCLASS_NAMES = ("gemm_bf16", "gemm_e4m3", "attention", "layernorm", "rmsnorm", "modulation",
@@ -159,6 +179,18 @@ _c = {
     "dlo_rmsnorm_bwd_workspace_bytes": _decl("dlo_rmsnorm_bwd_workspace_bytes", _sz, _int, _int),
     "dlo_op_rmsnorm_bwd": _decl("dlo_op_rmsnorm_bwd", _int, _vp, _int, _vp, _int, _vp, _vp, _int, _int, _vp, _int,
                                 _vp, _vp, _sz, _vp),
+    "dlo_op_packed_plan": _decl("dlo_op_packed_plan", _int, _vp, _vp, _int, _int, _int, _vp, _vp, _vp),
+    "dlo_rope_steps": _decl("dlo_rope_steps", _int, _P(dlo_rope), _vp, _int),
+    "dlo_op_rope_fwd": _decl("dlo_op_rope_fwd", _int, _P(dlo_rope), _vp, _vp, _vp, _int, _vp, _vp),
+    "dlo_op_rope_bwd": _decl("dlo_op_rope_bwd", _int, _P(dlo_rope), _vp, _vp, _vp, _int, _vp, _vp),
+    "dlo_attention_packed_fwd_workspace_bytes": _decl("dlo_attention_packed_fwd_workspace_bytes", _sz,
+                                                      _P(dlo_attn_packed)),
+    "dlo_attention_packed_bwd_workspace_bytes": _decl("dlo_attention_packed_bwd_workspace_bytes", _sz,
+                                                      _P(dlo_attn_packed)),
+    "dlo_op_attention_packed_fwd": _decl("dlo_op_attention_packed_fwd", _int, _P(dlo_attn_packed), _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _sz, _vp, _vp),
+    "dlo_op_attention_packed_bwd": _decl("dlo_op_attention_packed_bwd", _int, _P(dlo_attn_packed), _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _vp),
     "dlo_op_stage": _decl("dlo_op_stage", _int, _vp, _vp, _sz, _int, _vp),
 }
 
@@ -450,3 +482,59 @@ def dlo_rmsnorm_bwd_workspace_bytes(rows, D) -> int:
 
 def dlo_op_rmsnorm_bwd(dy, lddy, x, ldx, w, rstd, rows, D, dx, lddx, dw, ws, ws_bytes, stream) -> None:
     _check(_c["dlo_op_rmsnorm_bwd"](dy, lddy, x, ldx, w, rstd, rows, D, dx, lddx, dw, ws, ws_bytes, stream))
+
+
+# ------------------------------------------------------------------ packed batches
+
+def dlo_op_packed_plan(grids, offsets, batch, axes, rows, starts, positions, stream) -> None:
+    _check(_c["dlo_op_packed_plan"](grids, offsets, batch, axes, rows, starts, positions, stream))
+
+
+def make_rope(*, heads, head_dim, axes, ldx, ldy, layout=ROPE_INTERLEAVED, amp=1.0) -> dlo_rope:
+    """axes: one dict per axis with `dim` and, where they differ, theta (10000), scaling (ROPE_PLAIN), factor (1),
+    length, fast (32) and slow (1)."""
+    r = dlo_rope(heads=heads, head_dim=head_dim, layout=layout, axes=len(axes), ldx=ldx, ldy=ldy, amp=amp)
+    for i, a in enumerate(axes[:ROPE_AXES]):
+        r.axis[i] = dlo_rope_axis(**{**dict(scaling=ROPE_PLAIN, theta=10000.0, factor=1.0, length=0.0, fast=32.0, slow=1.0),
+                                     **a})
+    return r
+
+
+def dlo_rope_steps(r: dlo_rope):
+    """int64 array (the bits of the unsigned steps) of every pair of a head."""
+    import numpy as np
+    steps = np.zeros(sum(max(r.axis[i].dim, 0) // 2 for i in range(min(max(r.axes, 0), ROPE_AXES))), dtype=np.int64)
+    _check(_c["dlo_rope_steps"](ctypes.byref(r), steps.ctypes.data, steps.size))
+    return steps
+
+
+def dlo_op_rope_fwd(r: dlo_rope, x, positions, steps, rows, y, stream) -> None:
+    _check(_c["dlo_op_rope_fwd"](ctypes.byref(r), x, positions, steps, rows, y, stream))
+
+
+def dlo_op_rope_bwd(r: dlo_rope, dy, positions, steps, rows, dx, stream) -> None:
+    _check(_c["dlo_op_rope_bwd"](ctypes.byref(r), dy, positions, steps, rows, dx, stream))
+
+
+def make_attn_packed(*, batch, heads, head_dim, rows_q, rows_k, q_starts, k_starts, kv_heads=None, causal_block=0, ldq,
+                     ldk, ldv, ldo, lddq=0, lddk=0, lddv=0, lddo=0) -> dlo_attn_packed:
+    """q_starts, k_starts: device addresses of int32 [batch + 1] (kept alive by the caller)."""
+    return dlo_attn_packed(batch, heads, heads if kv_heads is None else kv_heads, head_dim, rows_q, rows_k, causal_block,
+                           ldq, ldk, ldv, ldo, lddq, lddk, lddv, lddo, q_starts, k_starts)
+
+
+def dlo_attention_packed_fwd_workspace_bytes(a: dlo_attn_packed) -> int:
+    return _size(_c["dlo_attention_packed_fwd_workspace_bytes"](ctypes.byref(a)))
+
+
+def dlo_attention_packed_bwd_workspace_bytes(a: dlo_attn_packed) -> int:
+    return _size(_c["dlo_attention_packed_bwd_workspace_bytes"](ctypes.byref(a)))
+
+
+def dlo_op_attention_packed_fwd(a: dlo_attn_packed, Q, K, V, O, lse, ws, ws_bytes, err, stream) -> None:
+    _check(_c["dlo_op_attention_packed_fwd"](ctypes.byref(a), Q, K, V, O, lse, ws, ws_bytes, err, stream))
+
+
+def dlo_op_attention_packed_bwd(a: dlo_attn_packed, Q, K, V, O, lse, dO, dQ, dK, dV, ws, ws_bytes, err, stream) -> None:
+    _check(_c["dlo_op_attention_packed_bwd"](ctypes.byref(a), Q, K, V, O, lse, dO, dQ, dK, dV, ws, ws_bytes, err,
+                                             stream))

@@ -52,9 +52,24 @@ __device__ __forceinline__ void store_tile(uint32_t src, const CUtensorMap* main
     if constexpr (TAIL) tma_store_4d(tail, src + NB * T::BLK, NB * 64, h, row0, b);
 }
 
+// The first `rows` rows of such a tile, in 16-byte pieces, by `step` threads, this
+// one the lane-th: tile row r to `out` + (r / gh) * ld + (r % gh) * hd.  For a tile
+// that ends inside a packed sequence's neighbour: TMA would write all of its box.
+template <int NB, bool TAIL>
+__device__ __forceinline__ void copy_rows(const uint8_t* tile, __nv_bfloat16* out, int ld, int rows, int gh, int hd, int lane, int step) {
+    using T = AttnTile<NB, TAIL>;
+    const int c8 = hd / 8;
+    for (int i = lane; i < rows * c8; i += step) {
+        const int r = i / c8, c = i - r * c8;
+        const uint8_t* from = !TAIL || c < 8 * NB ? tile + (c >> 3) * T::BLK + r * 128 + (((c & 7) ^ (r & 7)) << 4)
+                                                  : tile + NB * T::BLK + r * 32 + (((c & 1) ^ ((r >> 2) & 1)) << 4);
+        reinterpret_cast<uint4*>(out + static_cast<size_t>(r / gh) * ld + (r % gh) * hd)[c] = *reinterpret_cast<const uint4*>(from);
+    }
+}
+
 // [batch, rows, heads, hd] view of a bf16 matrix whose batch b, row r, head h
 // starts at base + (b * rows + r) * ld + h * hd; box of box_cols x box_heads
-// heads x 128 / box_heads rows, columns past hd zero-filled.
+// heads x (128 / box_heads rounded down) rows, columns past hd zero-filled.
 inline bool make_map4(CUtensorMap* m, const void* base, int batch, int rows, int heads, int hd, int ld,
                       int box_cols, CUtensorMapSwizzle sw, int box_heads = 1) {
     EncodeTiledFn enc = tensor_map_encoder();
@@ -97,6 +112,42 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane, int
 // may do so before its programmatic-launch wait.
 __device__ __forceinline__ int seq_len(const int* lens, int b, int n) {
     return lens ? min(max(__ldcg(lens + b), 0), n) : n;
+}
+
+// Packed sequences: sequence b is rows starts[b] .. starts[b + 1] - 1.  Tiles of t rows
+// that do not cross its ends have the slots from starts[b] / t + b on, of which the
+// next sequence's lie far enough: floor(s' / t) + 1 - floor(s / t) >= ceil((s' - s) / t).
+// So a grid of rows / t + batch slots finds its tiles in the starts alone, without a sum
+// over the lengths before it, and a slot too many a sequence finds none.
+struct PackedTile {
+    int b, tile;                // sequence and which of its tiles; tile < 0: none
+    int row0, n;                // the sequence's first row and its length
+};
+
+// starts[b] taken into 0 .. rows; L2, as seq_len.
+__device__ __forceinline__ int seq_start(const int* starts, int b, int rows) { return min(max(__ldcg(starts + b), 0), rows); }
+
+__host__ __device__ __forceinline__ int packed_slots(int rows, int batch, int t) { return rows / t + batch; }
+
+// The tile of a slot, by a whole warp: 32 sequences a step.
+__device__ __forceinline__ PackedTile packed_tile(const int* starts, int batch, int rows, int t, int slot) {
+    const int lane = threadIdx.x & 31;
+    int b = 0;
+    for (int n = batch; n > 1;) {           // it is one of b .. b + n - 1
+        const int step = (n + 31) / 32, i = b + lane * step;
+        const bool before = lane * step < n && seq_start(starts, i, rows) / t + i <= slot;
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, before);
+        const int k = m ? 31 - __clz(m) : 0;
+        b += k * step;
+        n = min(step, n - k * step);
+    }
+    PackedTile p;
+    p.b = b;
+    p.row0 = seq_start(starts, b, rows);
+    p.n = max(0, seq_start(starts, b + 1, rows) - p.row0);
+    p.tile = slot - (p.row0 / t + b);
+    if (static_cast<long long>(p.tile) * t >= p.n) p.tile = -1;
+    return p;
 }
 
 // One past the last key that query i sees (off = nk - nq, cb = causal block,

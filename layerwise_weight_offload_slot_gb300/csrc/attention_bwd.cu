@@ -42,6 +42,10 @@
 // D comes from the O that the forward wrote, in bf16, for rows of more than one key
 // tile; it is rowsum(P dP), without that rounding, for rows that lie in one.
 //
+// Packed sequences (PK): a CTA's tile, its rows and its mask are those of one
+// sequence (packed_tile), both lengths are known to it alone, and what it writes ends
+// with its sequence.
+//
 // P and dS are rounded to bf16 as operands of the tensor core (relative 2^-8
 // at most each, as P in the forward); every sum is fp32.  Every mbarrier wait is
 // bounded; one that runs out sets the error word, all roles leave their
@@ -69,12 +73,13 @@ struct BwdMaps {
 };
 
 struct BwdArgs {
-    const int *q_lens, *k_lens;
-    int nq, nk, hd, heads, group, causal_block;
+    const int *q_lens, *k_lens;   // PK: q_starts, k_starts
+    int nq, nk, hd, heads, group, causal_block;     // PK: nq, nk rows of all sequences
+    int batch;                    // PK
     float scale, scale_log2;      // 1 / sqrt(hd), log2(e) / sqrt(hd)
     const __nv_bfloat16 *O, *dO;
     const float* lse;
-    uint4* stats;                 // [batch * heads][query tiles] operands of kStatBytes
+    uint4* stats;                 // [batch * heads][query tiles] operands of kStatBytes; PK: [heads][slots]
     __nv_bfloat16 *dQ, *dK, *dV;
     int ldo, lddo, lddq, lddk, lddv;
     // CTAs that share one gradient tile, each a part of its products' other
@@ -329,7 +334,7 @@ __device__ __forceinline__ void write_stat(uint4* stat, int r, float neg_l, floa
 // so that they find their next operands ready.  Two warps issue, S and dP one, dQ
 // the other: each waits for its own barriers while the other's products run (a
 // tile at head dim 64: 0.74 us, against 0.84 with one).
-template <int NB, bool TAIL>
+template <int NB, bool TAIL, bool PK>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
     using P = BwdPlan<NB, TAIL, true>;
@@ -349,24 +354,40 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     // with a causal mask the last query tiles see the most keys: first
     const int qtiles = gridDim.x / g.splits_q, split = blockIdx.x % g.splits_q;
-    const int qt = qtiles - 1 - blockIdx.x / g.splits_q, h = blockIdx.y, b = blockIdx.z;
-    const int row0 = qt * kTile, off = g.nk - g.nq;
+    const int slot = qtiles - 1 - blockIdx.x / g.splits_q, h = blockIdx.y, b = blockIdx.z;
 
     pdl_wait();
-    const int qlen = seq_len(g.q_lens, b, g.nq), klen = seq_len(g.k_lens, b, g.nk);
+    int qt = slot, nq = g.nq, nk = g.nk, qlen, klen;      // of one sequence
+    int q0 = 0, k0 = 0;                                   // PK: its first rows
+    if constexpr (PK) {
+        const PackedTile p = packed_tile(g.q_lens, g.batch, g.nq, kTile, slot);
+        if (p.tile < 0) return;
+        qt = p.tile;
+        q0 = p.row0;
+        k0 = seq_start(g.k_lens, p.b, g.nk);
+        qlen = nq = p.n;
+        klen = nk = max(0, seq_start(g.k_lens, p.b + 1, g.nk) - k0);
+    } else {
+        qlen = seq_len(g.q_lens, b, nq);
+        klen = seq_len(g.k_lens, b, nk);
+    }
+    const int row0 = qt * kTile, off = nk - nq;
+    // the tile's first row in the matrices and in the row statistics
+    const size_t out0 = PK ? static_cast<size_t>(q0) + row0 : static_cast<size_t>(b) * nq + row0;
+    const size_t lse0 = PK ? static_cast<size_t>(h) * g.nq + q0 + row0 : (static_cast<size_t>(b) * g.heads + h) * nq + row0;
     const int last = min(row0 + kTile, qlen) - 1;
     const int all = last < row0 ? 0 : (key_end(last, off, g.causal_block, klen) + kTile - 1) / kTile;
     // key tiles [j0, j0 + n) are this CTA's
     const int per = (all + g.splits_q - 1) / g.splits_q, j0 = split * per, n = min(all, j0 + per) - j0;
-    uint4* stat = split ? nullptr : g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16);
-    __nv_bfloat16* dq0 = g.dQ + (static_cast<size_t>(b) * g.nq + row0) * g.lddq + h * g.hd;
+    uint4* stat = split ? nullptr : g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + slot) * (kStatBytes / 16);
+    __nv_bfloat16* dq0 = g.dQ + out0 * g.lddq + h * g.hd;
     const int ldp = g.heads * g.hd;
     float* part0 = g.splits_q == 1 ? nullptr
-                                   : g.part_q + ((static_cast<size_t>(split) * gridDim.z + b) * g.nq + row0) * ldp + h * g.hd;
+                                   : g.part_q + (static_cast<size_t>(split) * gridDim.z * g.nq + out0) * ldp + h * g.hd;
     if (n <= 0) {
         if (stat && threadIdx.x < kTile) write_stat(stat, threadIdx.x, kNothing, 0.f);
-        if (part0) zero_out(part0, ldp, min(kTile, g.nq - row0), g.hd);
-        else zero_out(dq0, g.lddq, min(kTile, g.nq - row0), g.hd);
+        if (part0) zero_out(part0, ldp, min(kTile, nq - row0), g.hd);
+        else zero_out(dq0, g.lddq, min(kTile, nq - row0), g.hd);
         return;
     }
 
@@ -385,12 +406,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         for (int u = 0; u < 8 / RP; ++u) {
             const int row = (warp - 4) * 8 + u * RP + lane / LP, c = lane % LP;
             const bool in = !one_tile && row0 + row < qlen && c < g.hd / 8;
-            const size_t r = static_cast<size_t>(b) * g.nq + row0 + row;
+            const size_t r = out0 + row;
             o[u] = in ? reinterpret_cast<const uint4*>(g.O + r * g.ldo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
             d[u] = in ? reinterpret_cast<const uint4*>(g.dO + r * g.lddo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
         }
-        const int i = row0 + (warp & 3) * 32 + lane;
-        if (i < qlen) l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
+        const int i = (warp & 3) * 32 + lane;
+        if (row0 + i < qlen) l = g.lse[lse0 + i];
     }
     if (threadIdx.x == 0) {
         bwd_init<P::SLOTS>(m, 1, 1);
@@ -398,8 +419,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         // this thread is also the one that loads: the first tiles need not wait
         // for the rest of the set-up
         mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
-        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, row0, b, m.a_full);
-        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, row0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, q0 + row0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, q0 + row0, b, m.a_full);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -422,7 +443,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     };
     // keys behind k_lens end inside the last tile: its K rows there become zero
     // before the MMAs see it (its loads complete on raw0 instead)
-    const int fix = klen < g.nk && klen < (j0 + n) * kTile ? klen - (j0 + n - 1) * kTile : kTile;
+    // (PK: the next sequence's rows)
+    const int fix = (PK || klen < nk) && klen < (j0 + n) * kTile ? klen - (j0 + n - 1) * kTile : kTile;
 
     if (warp == 0) {
         // ---------------- TMA: K and V
@@ -436,7 +458,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 const bool raw = fix < kTile && j == n - 1;
                 const uint32_t full = raw ? m.raw0 : m.full + 8 * k.s;
                 mbar_arrive_expect_tx(full, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R_OFF + k.s * P::TILE, &maps.k, &maps.kt, hk, (j0 + j) * kTile, b, full);
+                load_tile<NB, TAIL>(sb + P::R_OFF + k.s * P::TILE, &maps.k, &maps.kt, hk, k0 + (j0 + j) * kTile, b, full);
                 if (!raw) in.add(k);
                 if (!mbar_wait(m.empty + 8 * v.s, v.ph ^ 1, abort_flag)) {
                     ok = false;
@@ -444,7 +466,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                     break;
                 }
                 mbar_arrive_expect_tx(m.full + 8 * v.s, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R_OFF + v.s * P::TILE, &maps.v, &maps.vt, hk, (j0 + j) * kTile, b, m.full + 8 * v.s);
+                load_tile<NB, TAIL>(sb + P::R_OFF + v.s * P::TILE, &maps.v, &maps.vt, hk, k0 + (j0 + j) * kTile, b, m.full + 8 * v.s);
                 in.add(v);
             }
         }
@@ -617,17 +639,22 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         } else {
             tc_fence_after();
             // the slots' tiles have all been read: the first one takes the result
-            store_row<NB, TAIL>(tl + 384, smem + P::R_OFF, row, part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < g.nq,
+            store_row<NB, TAIL>(tl + 384, smem + P::R_OFF, row, part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < nq,
                                 end <= 0, g.scale, e, kGroups);
             if (!part0) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m.staged);
-                if (warp == 4) {
+                if (PK && nq - row0 < kTile) {
+                    if (warp_wait(m.staged, 0, abort_flag))
+                        copy_rows<NB, TAIL>(smem + P::R_OFF, dq0, g.lddq, nq - row0, 1, g.hd, threadIdx.x - 128, kThreadsB - 128);
+                    else if (lane == 0)
+                        fail();
+                } else if (warp == 4) {
                     ok = warp_wait(m.staged, 0, abort_flag);
                     if (lane == 0) {
                         if (ok) {
-                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gq, &maps.gqt, h, row0, b);
+                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gq, &maps.gqt, h, q0 + row0, b);
                             bulk_commit();
                             bulk_wait_all();
                         } else {
@@ -652,7 +679,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // TMEM: S^T [0, 128), dP^T [128, 256), then dV, dK and, where they fit, P^T and
 // dS^T; else these take the places of S^T and dP^T, and then dV_i goes before
 // S_{i+1} and dK_i before dP_{i+1} in one order of issue.
-template <int NB, bool TAIL>
+template <int NB, bool TAIL, bool PK>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
     using P = BwdPlan<NB, TAIL, false>;
@@ -671,9 +698,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         return;
     }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int kt = blockIdx.x / g.splits_k, split = blockIdx.x % g.splits_k, hk = blockIdx.y, b = blockIdx.z;
-    const int key0 = kt * kTile, off = g.nk - g.nq;
-    const int qtiles = (g.nq + kTile - 1) / kTile;
+    const int split = blockIdx.x % g.splits_k, hk = blockIdx.y, b = blockIdx.z;
+    int kt = blockIdx.x / g.splits_k;
+    int qtiles = PK ? packed_slots(g.nq, g.batch, kTile) : (g.nq + kTile - 1) / kTile;     // of a head's row statistics
 
     // This grid starts while dq_kernel, whose every CTA has waited for what came
     // before, ends: all inputs are there, and only the row statistics, dq_kernel's
@@ -681,26 +708,45 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // for this grid has waited for dq_kernel too.  (In a graph, 256 tokens of 4 heads
     // of 64: 10.1 us for the two launches, 11.3 with the wait here; 2 x 16 heads of
     // 72, 1024 tokens: 48.8, 50.4 with it.)
-    const int qlen = seq_len(g.q_lens, b, g.nq), klen = seq_len(g.k_lens, b, g.nk);
+    int nq = g.nq, nk = g.nk, qlen, klen;                 // of one sequence
+    int q0 = 0, k0 = 0, slot0 = 0;                        // PK: its first rows and the slot of its first query tile
+    if constexpr (PK) {
+        const PackedTile p = packed_tile(g.k_lens, g.batch, g.nk, kTile, kt);
+        if (p.tile < 0) {
+            pdl_wait();
+            return;
+        }
+        kt = p.tile;
+        k0 = p.row0;
+        q0 = seq_start(g.q_lens, p.b, g.nq);
+        klen = nk = p.n;
+        qlen = nq = max(0, seq_start(g.q_lens, p.b + 1, g.nq) - q0);
+        slot0 = q0 / kTile + p.b;
+    } else {
+        qlen = seq_len(g.q_lens, b, nq);
+        klen = seq_len(g.k_lens, b, nk);
+    }
+    const int key0 = kt * kTile, off = nk - nq;
+    const size_t out0 = PK ? static_cast<size_t>(k0) + key0 : static_cast<size_t>(b) * nk + key0;
     // query tiles [t0, t1) of each of the group's heads, one after the other
     const int t0 = max(0, query_begin(key0, off, g.causal_block)) / kTile;
     const int t1 = key0 < klen ? (qlen + kTile - 1) / kTile : 0;
     const int per = max(0, t1 - t0), all = per * g.group;
     // of these `all` steps, [i0, i0 + n) are this CTA's
     const int share = (all + g.splits_k - 1) / g.splits_k, i0 = split * share, n = min(all, i0 + share) - i0;
-    __nv_bfloat16* dk0 = g.dK + (static_cast<size_t>(b) * g.nk + key0) * g.lddk + hk * g.hd;
-    __nv_bfloat16* dv0 = g.dV + (static_cast<size_t>(b) * g.nk + key0) * g.lddv + hk * g.hd;
+    __nv_bfloat16* dk0 = g.dK + out0 * g.lddk + hk * g.hd;
+    __nv_bfloat16* dv0 = g.dV + out0 * g.lddv + hk * g.hd;
     const int ldp = gridDim.y * g.hd;
-    const size_t part_at = ((static_cast<size_t>(split) * gridDim.z + b) * g.nk + key0) * ldp + hk * g.hd;
+    const size_t part_at = (static_cast<size_t>(split) * gridDim.z * g.nk + out0) * ldp + hk * g.hd;
     const bool parts = g.splits_k > 1;
     if (n <= 0) {
         pdl_wait();
         if (parts) {
-            zero_out(g.part_k + part_at, ldp, min(kTile, g.nk - key0), g.hd);
-            zero_out(g.part_v + part_at, ldp, min(kTile, g.nk - key0), g.hd);
+            zero_out(g.part_k + part_at, ldp, min(kTile, nk - key0), g.hd);
+            zero_out(g.part_v + part_at, ldp, min(kTile, nk - key0), g.hd);
         } else {
-            zero_out(dk0, g.lddk, min(kTile, g.nk - key0), g.hd);
-            zero_out(dv0, g.lddv, min(kTile, g.nk - key0), g.hd);
+            zero_out(dk0, g.lddk, min(kTile, nk - key0), g.hd);
+            zero_out(dv0, g.lddv, min(kTile, nk - key0), g.hd);
         }
         return;
     }
@@ -709,8 +755,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         bwd_init<P::SLOTS>(m, M::ISSUERS, M::ISSUERS);
         *abort_flag = 0;
         mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
-        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, key0, b, m.a_full);
-        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.v, &maps.vt, hk, key0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, k0 + key0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.v, &maps.vt, hk, k0 + key0, b, m.a_full);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -741,7 +787,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     };
     // queries behind q_lens end inside each head's last tile: its Q and dO rows
     // there become zero before the MMAs see it (loads complete on raw0, raw1)
-    const int fix = qlen < g.nq && qlen < t1 * kTile ? qlen - (t1 - 1) * kTile : kTile;
+    // (PK: the next sequence's rows)
+    const int fix = (PK || qlen < nq) && qlen < t1 * kTile ? qlen - (t1 - 1) * kTile : kTile;
 
     if (warp == 0) {
         // ---------------- TMA: Q with the row statistics, and dO
@@ -757,15 +804,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 ok = mbar_wait(m.empty + 8 * q.s, q.ph ^ 1, abort_flag);
                 if (ok) {
                     mbar_arrive_expect_tx(full0, P::TILE + kStatBytes);
-                    load_tile<NB, TAIL>(sb + P::R_OFF + q.s * P::TILE, &maps.q, &maps.qt, h, qt * kTile, b, full0);
+                    load_tile<NB, TAIL>(sb + P::R_OFF + q.s * P::TILE, &maps.q, &maps.qt, h, q0 + qt * kTile, b, full0);
                     if (i == 0) pdl_wait();
                     bulk_load(sb + P::STAT_OFF + i % P::STATS * kStatBytes,
-                              g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16), kStatBytes, full0);
+                              g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + slot0 + qt) * (kStatBytes / 16), kStatBytes, full0);
                     if (!raw) in.add(q);
                     ok = mbar_wait(m.empty + 8 * d.s, d.ph ^ 1, abort_flag);
                     if (ok) {
                         mbar_arrive_expect_tx(full1, P::TILE);
-                        load_tile<NB, TAIL>(sb + P::R_OFF + d.s * P::TILE, &maps.d, &maps.dt, h, qt * kTile, b, full1);
+                        load_tile<NB, TAIL>(sb + P::R_OFF + d.s * P::TILE, &maps.d, &maps.dt, h, q0 + qt * kTile, b, full1);
                         if (!raw) in.add(d);
                     } else if (raw) {
                         mbar_wait(m.raw0, raws & 1, nullptr);
@@ -1007,18 +1054,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             // even groups bring dV, odd ones dK, into the first two slots
             const bool k = e & 1;
             float* part = parts ? (k ? g.part_k : g.part_v) + part_at + static_cast<size_t>(row) * ldp : nullptr;
-            store_row<NB, TAIL>(tl + (k ? M::DK_COL : M::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < g.nk,
+            store_row<NB, TAIL>(tl + (k ? M::DK_COL : M::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < nk,
                                 begin >= qlen, k ? g.scale : 1.f, e >> 1, kGroups / 2);
             if (!parts) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m.staged);
-                if (warp == 4) {
+                if (PK && nk - key0 < kTile) {
+                    if (warp_wait(m.staged, 0, abort_flag)) {
+                        copy_rows<NB, TAIL>(smem + P::R_OFF, dv0, g.lddv, nk - key0, 1, g.hd, threadIdx.x - 128, kThreadsB - 128);
+                        copy_rows<NB, TAIL>(smem + P::R_OFF + P::TILE, dk0, g.lddk, nk - key0, 1, g.hd, threadIdx.x - 128,
+                                            kThreadsB - 128);
+                    } else if (lane == 0) {
+                        fail();
+                    }
+                } else if (warp == 4) {
                     ok = warp_wait(m.staged, 0, abort_flag);
                     if (lane == 0) {
                         if (ok) {
-                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gv, &maps.gvt, hk, key0, b);
-                            store_tile<NB, TAIL>(sb + P::R_OFF + P::TILE, &maps.gk, &maps.gkt, hk, key0, b);
+                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gv, &maps.gvt, hk, k0 + key0, b);
+                            store_tile<NB, TAIL>(sb + P::R_OFF + P::TILE, &maps.gk, &maps.gkt, hk, k0 + key0, b);
                             bulk_commit();
                             bulk_wait_all();
                         } else {
@@ -1046,6 +1101,8 @@ struct JoinOne {
     __nv_bfloat16* out;
     int splits, ld, c8;          // c8: pieces of 8 columns a row
     long long rows;
+    const int* starts;           // packed: rows of no sequence stay as they are
+    int batch;
 };
 struct JoinArgs {
     JoinOne one[3];
@@ -1063,6 +1120,8 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ J
             i -= n;
             continue;
         }
+        const long long row = i / j.c8;
+        if (j.starts && (row < __ldcg(j.starts) || row >= __ldcg(j.starts + j.batch))) return;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         const float4* p = reinterpret_cast<const float4*>(j.part) + 2 * i;
 #pragma unroll 4
@@ -1071,7 +1130,6 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ J
             x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
             y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
         }
-        const long long row = i / j.c8;
         reinterpret_cast<uint4*>(j.out + row * j.ld)[i - row * j.c8] =
             make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
         return;
@@ -1089,9 +1147,11 @@ struct BwdSplit {
     size_t part_q, part_k, part_v, total;      // byte offsets
 };
 
-BwdSplit bwd_split(const dlo_attn& a) {
-    const long long qt = (a.nq + kTile - 1) / kTile, kt = (a.nk + kTile - 1) / kTile, group = a.heads / a.kv_heads;
-    const long long nq = qt * a.heads * a.batch, nk = kt * a.kv_heads * a.batch, steps = qt * group;
+// qt, kt: query and key tiles of a sequence (packed: of a mean one); tiles_q, tiles_k: of
+// all; rows_q, rows_k: of all.
+BwdSplit bwd_split(int heads, int kv_heads, int head_dim, bool causal, long long qt, long long kt, long long tiles_q,
+                   long long tiles_k, size_t rows_q, size_t rows_k) {
+    const long long nq = tiles_q * heads, nk = tiles_k * kv_heads, steps = qt * (heads / kv_heads);
     const auto fill = [](long long ctas, long long work) {
         long long s = kGb300Sms / ctas;
         if (s > work / 4) s = work / 4;
@@ -1099,7 +1159,7 @@ BwdSplit bwd_split(const dlo_attn& a) {
     };
     BwdSplit b;
     long long sq = fill(nq, kt), sk = fill(nk, steps);
-    if (a.causal_block > 0) {
+    if (causal) {
         // about half of all steps are done
         const long long mean = nk * steps / 2 / kGb300Sms + 1;
         long long s = (steps + mean - 1) / mean;
@@ -1108,99 +1168,139 @@ BwdSplit bwd_split(const dlo_attn& a) {
     }
     b.q = static_cast<int>(sq);
     b.k = static_cast<int>(sk);
-    const size_t rq = static_cast<size_t>(a.batch) * a.nq * a.heads * a.head_dim * sizeof(float);
-    const size_t rk = static_cast<size_t>(a.batch) * a.nk * a.kv_heads * a.head_dim * sizeof(float);
-    b.part_q = static_cast<size_t>(a.batch) * a.heads * qt * kStatBytes;
+    const size_t rq = rows_q * heads * head_dim * sizeof(float), rk = rows_k * kv_heads * head_dim * sizeof(float);
+    b.part_q = static_cast<size_t>(tiles_q) * heads * kStatBytes;
     b.part_k = b.part_q + (b.q > 1 ? b.q * rq : 0);
     b.part_v = b.part_k + (b.k > 1 ? b.k * rk : 0);
     b.total = b.part_v + (b.k > 1 ? b.k * rk : 0);
     return b;
 }
 
-template <int NB, bool TAIL>
+BwdSplit bwd_split(const dlo_attn& a) {
+    const long long qt = (a.nq + kTile - 1) / kTile, kt = (a.nk + kTile - 1) / kTile;
+    return bwd_split(a.heads, a.kv_heads, a.head_dim, a.causal_block > 0, qt, kt, qt * a.batch, kt * a.batch,
+                     static_cast<size_t>(a.batch) * a.nq, static_cast<size_t>(a.batch) * a.nk);
+}
+
+BwdSplit bwd_split(const dlo_attn_packed& a) {
+    return bwd_split(a.heads, a.kv_heads, a.head_dim, a.causal_block > 0, (a.rows_q / a.batch + kTile) / kTile,
+                     (a.rows_k / a.batch + kTile) / kTile, packed_slots(a.rows_q, a.batch, kTile),
+                     packed_slots(a.rows_k, a.batch, kTile), a.rows_q, a.rows_k);
+}
+
+template <int NB, bool TAIL, bool PACKED>
 cudaError_t run_bwd(const BwdMaps& maps, const BwdArgs& g, int batch, int kv_heads, cudaStream_t s,
                     unsigned long long* launches) {
     using PQ = BwdPlan<NB, TAIL, true>;
     using PK = BwdPlan<NB, TAIL, false>;
+    constexpr auto dq = dq_kernel<NB, TAIL, PACKED>;
+    constexpr auto dkv = dkv_kernel<NB, TAIL, PACKED>;
     static unsigned long long set[2] = {0, 0};
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dq_kernel<NB, TAIL>), PQ::BYTES, &set[0]); e != cudaSuccess) return e;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dkv_kernel<NB, TAIL>), PK::BYTES, &set[1]); e != cudaSuccess) return e;
-    cudaError_t e = launch_k(dq_kernel<NB, TAIL>, dim3((g.nq + kTile - 1) / kTile * g.splits_q, g.heads, batch), kThreadsB, PQ::BYTES, s, maps, g);
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(dq), PQ::BYTES, &set[0]); e != cudaSuccess) return e;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(dkv), PK::BYTES, &set[1]); e != cudaSuccess) return e;
+    const int tq = PACKED ? packed_slots(g.nq, g.batch, kTile) : (g.nq + kTile - 1) / kTile;
+    const int tk = PACKED ? packed_slots(g.nk, g.batch, kTile) : (g.nk + kTile - 1) / kTile;
+    cudaError_t e = launch_k(dq, dim3(tq * g.splits_q, g.heads, batch), kThreadsB, PQ::BYTES, s, maps, g);
     ++*launches;
     if (e != cudaSuccess) return e;
-    e = launch_k(dkv_kernel<NB, TAIL>, dim3((g.nk + kTile - 1) / kTile * g.splits_k, kv_heads, batch), kThreadsB, PK::BYTES, s, maps, g);
+    e = launch_k(dkv, dim3(tk * g.splits_k, kv_heads, batch), kThreadsB, PK::BYTES, s, maps, g);
+    ++*launches;
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+struct BwdPointers {
+    const void *Q, *K, *V, *O;
+    const float* lse;
+    const void* dO;
+    void *dQ, *dK, *dV, *ws;
+    int* err;
+};
+
+// Both forms, whose descriptions name the same things: `batch` sequences of nq and nk
+// rows, or (PACKED) one of all rows.
+template <bool PACKED, typename Attn>
+cudaError_t launch_bwd(const Attn& a, int batch, int nq, int nk, const int* q_seq, const int* k_seq, const BwdPointers& p,
+                       cudaStream_t s, unsigned long long* launches) {
+    const int hd = a.head_dim;
+    BwdArgs g = {};
+    g.q_lens = q_seq;
+    g.k_lens = k_seq;
+    g.nq = nq;
+    g.nk = nk;
+    g.batch = a.batch;
+    g.hd = hd;
+    g.heads = a.heads;
+    g.group = a.heads / a.kv_heads;
+    g.causal_block = a.causal_block < nk ? a.causal_block : nk;
+    g.scale = 1.f / sqrtf(static_cast<float>(hd));
+    g.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
+    g.O = static_cast<const __nv_bfloat16*>(p.O);
+    g.dO = static_cast<const __nv_bfloat16*>(p.dO);
+    g.lse = p.lse;
+    g.stats = static_cast<uint4*>(p.ws);
+    const BwdSplit split = bwd_split(a);
+    uint8_t* base = static_cast<uint8_t*>(p.ws);
+    g.splits_q = split.q;
+    g.splits_k = split.k;
+    g.part_q = reinterpret_cast<float*>(base + split.part_q);
+    g.part_k = reinterpret_cast<float*>(base + split.part_k);
+    g.part_v = reinterpret_cast<float*>(base + split.part_v);
+    g.dQ = static_cast<__nv_bfloat16*>(p.dQ);
+    g.dK = static_cast<__nv_bfloat16*>(p.dK);
+    g.dV = static_cast<__nv_bfloat16*>(p.dV);
+    g.ldo = a.ldo;
+    g.lddo = a.lddo;
+    g.lddq = a.lddq;
+    g.lddk = a.lddk;
+    g.lddv = a.lddv;
+    g.err = p.err;
+    BwdMaps m;
+    const CUtensorMapSwizzle w128 = CU_TENSOR_MAP_SWIZZLE_128B, w32 = CU_TENSOR_MAP_SWIZZLE_32B;
+    const bool tail = hd > 64 && hd <= 80;
+    auto map = [&](CUtensorMap* main, CUtensorMap* tl, const void* q, int rows, int heads, int ld) {
+        if (!make_map4(main, q, batch, rows, heads, hd, ld, 64, w128)) return false;
+        if (tail) return make_map4(tl, q, batch, rows, heads, hd, ld, 16, w32);
+        *tl = *main;
+        return true;
+    };
+    if (!map(&m.q, &m.qt, p.Q, nq, a.heads, a.ldq) || !map(&m.k, &m.kt, p.K, nk, a.kv_heads, a.ldk) ||
+        !map(&m.v, &m.vt, p.V, nk, a.kv_heads, a.ldv) || !map(&m.d, &m.dt, p.dO, nq, a.heads, a.lddo) ||
+        !map(&m.gq, &m.gqt, p.dQ, nq, a.heads, a.lddq) || !map(&m.gk, &m.gkt, p.dK, nk, a.kv_heads, a.lddk) ||
+        !map(&m.gv, &m.gvt, p.dV, nk, a.kv_heads, a.lddv))
+        return cudaErrorInvalidValue;
+    cudaError_t e = hd <= 64 ? run_bwd<1, false, PACKED>(m, g, batch, a.kv_heads, s, launches)
+                    : tail   ? run_bwd<1, true, PACKED>(m, g, batch, a.kv_heads, s, launches)
+                             : run_bwd<2, false, PACKED>(m, g, batch, a.kv_heads, s, launches);
+    if (e != cudaSuccess || (split.q == 1 && split.k == 1)) return e;
+    const long long rq = static_cast<long long>(batch) * nq, rk = static_cast<long long>(batch) * nk;
+    const int cq = a.heads * hd / 8, ck = a.kv_heads * hd / 8;
+    const int *sq = PACKED ? q_seq : nullptr, *sk = PACKED ? k_seq : nullptr;
+    const JoinArgs j = {{{g.part_q, g.dQ, split.q, a.lddq, cq, split.q > 1 ? rq : 0, sq, a.batch},
+                         {g.part_k, g.dK, split.k, a.lddk, ck, split.k > 1 ? rk : 0, sk, a.batch},
+                         {g.part_v, g.dV, split.k, a.lddv, ck, split.k > 1 ? rk : 0, sk, a.batch}}};
+    const long long n = j.one[0].rows * cq + 2 * j.one[1].rows * ck;
+    e = launch_k(bwd_join_kernel, static_cast<unsigned>((n + 255) / 256), 256, 0, s, j);
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attention_bwd_workspace(const dlo_attn& a) {
-    return bwd_split(a).total;
-}
+size_t attention_bwd_workspace(const dlo_attn& a) { return bwd_split(a).total; }
+
+size_t attention_packed_bwd_workspace(const dlo_attn_packed& a) { return bwd_split(a).total; }
 
 cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K, const void* V, const void* O,
                                  const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
                                  cudaStream_t s, unsigned long long* launches) {
-    const int hd = a.head_dim;
-    BwdArgs g = {};
-    g.q_lens = a.q_lens;
-    g.k_lens = a.k_lens;
-    g.nq = a.nq;
-    g.nk = a.nk;
-    g.hd = hd;
-    g.heads = a.heads;
-    g.group = a.heads / a.kv_heads;
-    g.causal_block = a.causal_block < a.nk ? a.causal_block : a.nk;
-    g.scale = 1.f / sqrtf(static_cast<float>(hd));
-    g.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
-    g.O = static_cast<const __nv_bfloat16*>(O);
-    g.dO = static_cast<const __nv_bfloat16*>(dO);
-    g.lse = lse;
-    g.stats = static_cast<uint4*>(ws);
-    const BwdSplit split = bwd_split(a);
-    uint8_t* base = static_cast<uint8_t*>(ws);
-    g.splits_q = split.q;
-    g.splits_k = split.k;
-    g.part_q = reinterpret_cast<float*>(base + split.part_q);
-    g.part_k = reinterpret_cast<float*>(base + split.part_k);
-    g.part_v = reinterpret_cast<float*>(base + split.part_v);
-    g.dQ = static_cast<__nv_bfloat16*>(dQ);
-    g.dK = static_cast<__nv_bfloat16*>(dK);
-    g.dV = static_cast<__nv_bfloat16*>(dV);
-    g.ldo = a.ldo;
-    g.lddo = a.lddo;
-    g.lddq = a.lddq;
-    g.lddk = a.lddk;
-    g.lddv = a.lddv;
-    g.err = err;
-    BwdMaps m;
-    const CUtensorMapSwizzle w128 = CU_TENSOR_MAP_SWIZZLE_128B, w32 = CU_TENSOR_MAP_SWIZZLE_32B;
-    const bool tail = hd > 64 && hd <= 80;
-    auto map = [&](CUtensorMap* main, CUtensorMap* tl, const void* p, int rows, int heads, int ld) {
-        if (!make_map4(main, p, a.batch, rows, heads, hd, ld, 64, w128)) return false;
-        if (tail) return make_map4(tl, p, a.batch, rows, heads, hd, ld, 16, w32);
-        *tl = *main;
-        return true;
-    };
-    if (!map(&m.q, &m.qt, Q, a.nq, a.heads, a.ldq) || !map(&m.k, &m.kt, K, a.nk, a.kv_heads, a.ldk) ||
-        !map(&m.v, &m.vt, V, a.nk, a.kv_heads, a.ldv) || !map(&m.d, &m.dt, dO, a.nq, a.heads, a.lddo) ||
-        !map(&m.gq, &m.gqt, dQ, a.nq, a.heads, a.lddq) || !map(&m.gk, &m.gkt, dK, a.nk, a.kv_heads, a.lddk) ||
-        !map(&m.gv, &m.gvt, dV, a.nk, a.kv_heads, a.lddv))
-        return cudaErrorInvalidValue;
-    cudaError_t e = hd <= 64 ? run_bwd<1, false>(m, g, a.batch, a.kv_heads, s, launches)
-                    : tail   ? run_bwd<1, true>(m, g, a.batch, a.kv_heads, s, launches)
-                             : run_bwd<2, false>(m, g, a.batch, a.kv_heads, s, launches);
-    if (e != cudaSuccess || (split.q == 1 && split.k == 1)) return e;
-    const long long rq = static_cast<long long>(a.batch) * a.nq, rk = static_cast<long long>(a.batch) * a.nk;
-    const int cq = a.heads * hd / 8, ck = a.kv_heads * hd / 8;
-    const JoinArgs j = {{{g.part_q, g.dQ, split.q, a.lddq, cq, split.q > 1 ? rq : 0},
-                         {g.part_k, g.dK, split.k, a.lddk, ck, split.k > 1 ? rk : 0},
-                         {g.part_v, g.dV, split.k, a.lddv, ck, split.k > 1 ? rk : 0}}};
-    const long long n = j.one[0].rows * cq + 2 * j.one[1].rows * ck;
-    e = launch_k(bwd_join_kernel, static_cast<unsigned>((n + 255) / 256), 256, 0, s, j);
-    ++*launches;
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return launch_bwd<false>(a, a.batch, a.nq, a.nk, a.q_lens, a.k_lens, {Q, K, V, O, lse, dO, dQ, dK, dV, ws, err}, s, launches);
+}
+
+cudaError_t launch_attention_packed_bwd(const dlo_attn_packed& a, const void* Q, const void* K, const void* V, const void* O,
+                                        const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
+                                        cudaStream_t s, unsigned long long* launches) {
+    return launch_bwd<true>(a, 1, a.rows_q, a.rows_k, a.q_starts, a.k_starts, {Q, K, V, O, lse, dO, dQ, dK, dV, ws, err}, s,
+                            launches);
 }
 
 }  // namespace dlo

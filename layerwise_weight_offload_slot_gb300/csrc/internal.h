@@ -255,4 +255,18 @@ cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K
                                  const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
                                  cudaStream_t s, unsigned long long* launches);
 
+// Operators for packed batches (attention_tc.cu, attention_bwd.cu, packed.cu).
+size_t attention_packed_fwd_workspace(const dlo_attn_packed& a);
+size_t attention_packed_bwd_workspace(const dlo_attn_packed& a);
+cudaError_t launch_attention_packed_fwd(const dlo_attn_packed& a, const void* Q, const void* K, const void* V, void* O,
+                                        float* lse, void* ws, int* err, cudaStream_t s, unsigned long long* launches);
+cudaError_t launch_attention_packed_bwd(const dlo_attn_packed& a, const void* Q, const void* K, const void* V, const void* O,
+                                        const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
+                                        cudaStream_t s, unsigned long long* launches);
+cudaError_t launch_packed_plan(const int* grids, const int* offsets, int batch, int axes, int rows, int* starts,
+                               int* positions, cudaStream_t s, unsigned long long* launches);
+// x rotated by its positions into y, or (back) by the opposite angles.
+cudaError_t launch_rope(const dlo_rope& r, bool back, const void* x, int ldx, const int* positions, const uint64_t* steps,
+                        int rows, void* y, int ldy, cudaStream_t s, unsigned long long* launches);
+
 }  // namespace dlo
