@@ -24,7 +24,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdlo.so")
 
 SOURCES = ["layout.cpp", "context.cpp", "train_ops.cpp", "packed_ops.cpp", "kernels_misc.cu", "norm_train.cu",
-           "gemm_tc.cu", "attention_tc.cu", "attention_bwd.cu", "packed.cu"]
+           "gemm_tc.cu", "attention_tc.cu", "attention_bwd.cu", "attention_packed.cu",
+           "attention_packed_bwd.cu", "packed.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-ffp-contract=off",
          "-I" + INCLUDE, "-I" + CSRC]

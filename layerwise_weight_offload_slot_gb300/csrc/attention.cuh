@@ -52,21 +52,6 @@ __device__ __forceinline__ void store_tile(uint32_t src, const CUtensorMap* main
     if constexpr (TAIL) tma_store_4d(tail, src + NB * T::BLK, NB * 64, h, row0, b);
 }
 
-// The first `rows` rows of such a tile, in 16-byte pieces, by `step` threads, this
-// one the lane-th: tile row r to `out` + (r / gh) * ld + (r % gh) * hd.  For a tile
-// that ends inside a packed sequence's neighbour: TMA would write all of its box.
-template <int NB, bool TAIL>
-__device__ __forceinline__ void copy_rows(const uint8_t* tile, __nv_bfloat16* out, int ld, int rows, int gh, int hd, int lane, int step) {
-    using T = AttnTile<NB, TAIL>;
-    const int c8 = hd / 8;
-    for (int i = lane; i < rows * c8; i += step) {
-        const int r = i / c8, c = i - r * c8;
-        const uint8_t* from = !TAIL || c < 8 * NB ? tile + (c >> 3) * T::BLK + r * 128 + (((c & 7) ^ (r & 7)) << 4)
-                                                  : tile + NB * T::BLK + r * 32 + (((c & 1) ^ ((r >> 2) & 1)) << 4);
-        reinterpret_cast<uint4*>(out + static_cast<size_t>(r / gh) * ld + (r % gh) * hd)[c] = *reinterpret_cast<const uint4*>(from);
-    }
-}
-
 // [batch, rows, heads, hd] view of a bf16 matrix whose batch b, row r, head h
 // starts at base + (b * rows + r) * ld + h * hd; box of box_cols x box_heads
 // heads x (128 / box_heads rounded down) rows, columns past hd zero-filled.
@@ -91,20 +76,23 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
     return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort));
 }
 
-// Rows [from, 128) of a tile set to zero by `step` threads, this one the lane-th.  Rows behind a sequence's
+// Lane 0's value.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
+
+// Rows [from, to) of a tile set to zero by `step` threads, this one the lane-th.  Rows behind a sequence's
 // end may hold anything; as the contracted index of a product they would turn
 // a zero probability times an infinity into NaN.  The caller's mbarrier arrival
 // after this orders the writes (async proxy) before the MMA that reads them.
 template <int NB, bool TAIL>
-__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane, int step) {
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int from, int lane, int step, int to = 128) {
     using T = AttnTile<NB, TAIL>;
     const uint4 z = make_uint4(0, 0, 0, 0);
-    for (int i = from * 8 + lane; i < 128 * 8; i += step) {
+    for (int i = from * 8 + lane; i < to * 8; i += step) {
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) reinterpret_cast<uint4*>(tile + blk * T::BLK)[i] = z;
     }
     if constexpr (TAIL)
-        for (int i = from * 2 + lane; i < 128 * 2; i += step) reinterpret_cast<uint4*>(tile + NB * T::BLK)[i] = z;
+        for (int i = from * 2 + lane; i < to * 2; i += step) reinterpret_cast<uint4*>(tile + NB * T::BLK)[i] = z;
     fence_proxy_async_smem();
 }
 
@@ -129,25 +117,36 @@ __device__ __forceinline__ int seq_start(const int* starts, int b, int rows) { r
 
 __host__ __device__ __forceinline__ int packed_slots(int rows, int batch, int t) { return rows / t + batch; }
 
-// The tile of a slot, by a whole warp: 32 sequences a step.
+// The tile of a slot, by a whole warp: 31 sequences a step, with the start of the
+// next one beside them (one trip to L2 for up to 31 sequences).
 __device__ __forceinline__ PackedTile packed_tile(const int* starts, int batch, int rows, int t, int slot) {
     const int lane = threadIdx.x & 31;
-    int b = 0;
-    for (int n = batch; n > 1;) {           // it is one of b .. b + n - 1
-        const int step = (n + 31) / 32, i = b + lane * step;
-        const bool before = lane * step < n && seq_start(starts, i, rows) / t + i <= slot;
-        const unsigned m = __ballot_sync(0xFFFFFFFFu, before);
+    PackedTile p;
+    p.b = 0;
+    for (int n = batch;;) {                 // it is one of b .. b + n - 1
+        const int step = (n + 30) / 31, i = p.b + min(lane * step, n);
+        const int s = seq_start(starts, i, rows);
+        const unsigned m = __ballot_sync(0xFFFFFFFFu, lane * step < n && s / t + i <= slot);
         const int k = m ? 31 - __clz(m) : 0;
-        b += k * step;
+        if (step == 1) {
+            p.b += k;
+            p.row0 = __shfl_sync(0xFFFFFFFFu, s, k);
+            p.n = max(0, __shfl_sync(0xFFFFFFFFu, s, k + 1) - p.row0);
+            break;
+        }
+        p.b += k * step;
         n = min(step, n - k * step);
     }
-    PackedTile p;
-    p.b = b;
-    p.row0 = seq_start(starts, b, rows);
-    p.n = max(0, seq_start(starts, b + 1, rows) - p.row0);
-    p.tile = slot - (p.row0 / t + b);
+    p.tile = slot - (p.row0 / t + p.b);
     if (static_cast<long long>(p.tile) * t >= p.n) p.tile = -1;
     return p;
+}
+
+// Rows of sequence b of the other matrix: its first row and length.  `same`: it is packed
+// as the one that the tile was found in.
+__device__ __forceinline__ void packed_other(const int* starts, int b, int rows, bool same, const PackedTile& p, int& row0, int& n) {
+    row0 = same ? p.row0 : seq_start(starts, b, rows);
+    n = same ? p.n : max(0, seq_start(starts, b + 1, rows) - row0);
 }
 
 // One past the last key that query i sees (off = nk - nq, cb = causal block,

@@ -42,44 +42,23 @@
 // D comes from the O that the forward wrote, in bf16, for rows of more than one key
 // tile; it is rowsum(P dP), without that rounding, for rows that lie in one.
 //
-// Packed sequences (PK): a CTA's tile, its rows and its mask are those of one
-// sequence (packed_tile), both lengths are known to it alone, and what it writes ends
-// with its sequence.
-//
 // P and dS are rounded to bf16 as operands of the tensor core (relative 2^-8
 // at most each, as P in the forward); every sum is fp32.  Every mbarrier wait is
 // bounded; one that runs out sets the error word, all roles leave their
 // loops, loads and MMAs in flight are drained and TMEM is freed.
-#include "attention.cuh"
+#include "attention_bwd.cuh"
 
 namespace dlo {
 
 namespace {
 
-constexpr int kTile = 128;
-constexpr int kGroups = 4;                               // warps that share 32 TMEM lanes
-constexpr int kCols = kTile / kGroups;                   // columns of each
-constexpr int kThreadsB = 128 + 32 * 4 * kGroups;
-// Row statistics of one query tile as the operand of one more step of 16 of a
-// product: 128 rows x 16 bf16 (32-byte rows, 32-byte swizzle), columns 0..2 the
-// three bf16 parts of -L, 3..5 those of -D.
-constexpr int kStatBytes = kTile * 32;
-
-struct BwdMaps {
-    CUtensorMap q, k, v, d;       // 64-column boxes, 128-byte swizzle (d: dO)
-    CUtensorMap qt, kt, vt, dt;   // 16-column tails, 32-byte swizzle
-    CUtensorMap gq, gk, gv;       // the gradients, likewise
-    CUtensorMap gqt, gkt, gvt;
-};
-
 struct BwdArgs {
-    const int *q_lens, *k_lens;   // PK: q_starts, k_starts
-    int nq, nk, hd, heads, group, causal_block;     // PK: nq, nk rows of all sequences
-    int batch;                    // PK
+    const int *q_lens, *k_lens;
+    int nq, nk, hd, heads, group, causal_block;
     float scale, scale_log2;      // 1 / sqrt(hd), log2(e) / sqrt(hd)
     const __nv_bfloat16 *O, *dO;
     const float* lse;
-    uint4* stats;                 // [batch * heads][query tiles] operands of kStatBytes; PK: [heads][slots]
+    uint4* stats;                 // [batch * heads][query tiles] operands of kStatBytes
     __nv_bfloat16 *dQ, *dK, *dV;
     int ldo, lddo, lddq, lddk, lddv;
     // CTAs that share one gradient tile, each a part of its products' other
@@ -88,193 +67,6 @@ struct BwdArgs {
     float *part_q, *part_k, *part_v;
     int* err;
 };
-
-// Shared memory of one CTA: two tiles that stay (Q and dO; K and V), slots for the
-// two streams of tiles that move (K and V; Q and dO), and per-row values.
-//
-// A reload takes ~1 us (2000 cycles) from L2, longer than an iteration's
-// products.  Tile i of the first stream (K in dq_kernel, Q in dkv_kernel) is
-// held from its first product to the last one of its iteration, one of the
-// second (V, dO) for a shorter time.  Up to head dim 80 each stream has three
-// slots.  Above, the two streams share five (dq) or four (dkv) slots so that
-// the earlier freed tile makes room for the tile needed sooner: slot s holds
-// first-stream tile s, then second-stream tile s + SLOTS - 2, then first-stream
-// tile s + SLOTS, ... (slots 2.. begin with the second stream).  Against separate
-// 3 + 2 and 2 + 2 rings this leaves a reload 4/3 (dq) and 1 (dkv) iterations.
-struct Slot {
-    int s;
-    uint32_t ph;              // parity of this use of the slot's barriers
-};
-
-template <int SLOTS, bool SHARED, bool SECOND>
-__device__ __forceinline__ Slot slot_of(int i) {
-    if constexpr (SHARED) {
-        const int r = i % SLOTS;
-        return SECOND ? Slot{(i + 2) % SLOTS, r >= SLOTS - 2 ? 1u : 0u} : Slot{r, r >= 2 ? 1u : 0u};
-    } else {
-        constexpr int N = SLOTS / 2;
-        return {i % N + (SECOND ? N : 0), static_cast<uint32_t>(i / N) & 1u};
-    }
-}
-
-template <int NB, bool TAIL, bool DQ>
-struct BwdPlan {
-    using T = AttnTile<NB, TAIL>;
-    static constexpr int TILE = T::BYTES;
-    static constexpr bool SHARED = NB == 2;
-    static constexpr int SLOTS = SHARED ? (DQ ? 5 : 4) : 6;
-    static constexpr int STATS = SHARED ? 2 : 3;            // statistics operands of dkv_kernel, tile i in i % STATS
-    static constexpr int A0_OFF = 0, A1_OFF = TILE;
-    static constexpr int R_OFF = 2 * TILE;
-    // dq: D of each row and four parts of it; dkv: the two selecting operands, then
-    // the statistics
-    static constexpr int SEL_OFF = R_OFF + SLOTS * TILE;
-    static constexpr int STAT_OFF = SEL_OFF + 2 * kStatBytes;
-    static constexpr int BAR_OFF = DQ ? SEL_OFF + (1 + kGroups) * kTile * 4 : STAT_OFF + STATS * kStatBytes;
-    // a_full, raw0, raw1, s_full, drain2, d_full, e0, e1, done, drain, s_read, d_read, staged; full, empty [SLOTS]
-    static constexpr int NBARS = 13 + 2 * SLOTS;
-    static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
-    static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
-    static constexpr int USED = ABORT_OFF + 4;
-    // one CTA per SM (it owns all 512 TMEM columns); 1 KB to align the base
-    // where there is room, else the kernel checks that the base is aligned
-    static constexpr int WANT = USED + 1024 > 118784 ? USED + 1024 : 118784;
-    static constexpr int BYTES = WANT < 227 * 1024 ? WANT : 227 * 1024;
-    static_assert(USED <= 227 * 1024, "attention backward shared memory plan exceeds 227 KB");
-};
-
-// dkv_kernel's tensor memory: S^T [0, 128), dP^T [128, 256), then dV and dK, then P^T
-// and dS^T (64 columns each) where 512 columns hold them.  A P or dS that
-// takes the place of its product instead makes the next product wait for it.
-template <int HDP>
-struct DkvTmem {
-    static constexpr uint32_t DV_COL = 256, DK_COL = DV_COL + HDP;
-    static constexpr uint32_t FREE = 512 - DK_COL - HDP;
-    static constexpr bool P_APART = FREE >= 64, DS_APART = FREE >= 128;
-    static constexpr uint32_t P_COL = P_APART ? DK_COL + HDP : 0;
-    static constexpr uint32_t DS_COL = DS_APART ? P_COL + 64 : 128;
-    // Issuing warps of dkv_kernel.  Two (S and dV; dP and dK) keep the tensor core
-    // fed while one waits: at head dim 64 (72) a tile takes 0.90 (1.11) us against
-    // 1.09 (1.27).  Where P and dS lie in the places of S and dP, each product
-    // has to wait for one of the other kind and the order of issue counts: one
-    // (head dim 128: 1.34 against 1.56).
-    static constexpr int ISSUERS = P_APART ? 2 : 1;
-    static_assert(DK_COL + HDP <= 512, "attention backward tensor memory plan");
-};
-
-struct BwdBars {
-    uint32_t a_full, raw0, raw1, s_full, drain2, d_full, e0, e1, done, drain, s_read, d_read, staged, full, empty;
-};
-
-template <int SLOTS>
-__device__ __forceinline__ BwdBars bwd_bars(uint32_t b) {
-    return {b, b + 8, b + 16, b + 24, b + 32, b + 40, b + 48, b + 56, b + 64, b + 72, b + 80, b + 88,
-            b + 96, b + 104, b + 104 + 8 * SLOTS};
-}
-
-template <int SLOTS>
-__device__ __forceinline__ void bwd_init(const BwdBars& m, int done, int readers) {
-    mbar_init(m.a_full, 1);
-    mbar_init(m.raw0, 1);
-    mbar_init(m.raw1, 1);
-    mbar_init(m.s_full, 1);
-    mbar_init(m.d_full, 1);
-    mbar_init(m.e0, 4 * kGroups);
-    mbar_init(m.e1, 4 * kGroups);
-    mbar_init(m.s_read, 4 * kGroups);
-    mbar_init(m.d_read, 4 * kGroups);
-    mbar_init(m.staged, 4 * kGroups);
-    mbar_init(m.done, done);
-    mbar_init(m.drain, 1);
-    mbar_init(m.drain2, 1);
-    for (int i = 0; i < SLOTS; ++i) {
-        mbar_init(m.full + 8 * i, 1);
-        mbar_init(m.empty + 8 * i, readers);
-    }
-    fence_mbar_init();
-}
-
-// Loads in flight, for the drain: slots and the parity of each.
-struct InFlight {
-    uint32_t on = 0, par = 0;
-    __device__ void add(Slot s) {
-        on |= 1u << s.s;
-        par = (par & ~(1u << s.s)) | (s.ph << s.s);
-    }
-    template <int SLOTS>
-    __device__ void drain(uint32_t full) const {
-        for (int i = 0; i < SLOTS; ++i)
-            if (on & (1u << i)) mbar_wait(full + 8 * i, (par >> i) & 1u, nullptr);
-    }
-};
-
-// 128 x 128 (+)= A B^T over the head dim, both operands K-major in shared memory.
-template <int NB, bool TAIL>
-__device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t at, uint64_t b, uint64_t bt) {
-    using T = AttnTile<NB, TAIL>;
-    constexpr uint32_t id = idesc_bf16_f32(kTile, kTile);
-#pragma unroll
-    for (int kk = 0; kk < NB * 4; ++kk) {
-        const uint32_t off = ((kk >> 2) * T::BLK + (kk & 3) * 32) >> 4;
-        tc_mma_f16(d, a + off, b + off, id, kk > 0);
-    }
-    if constexpr (TAIL) tc_mma_f16(d, at, bt, id, 1u);
-}
-
-// 128 x hd += A B: A in TMEM (bf16 pairs: the kCols contracted indices of group
-// e at a + GAP e), B a tile of shared memory whose rows are the contracted index.
-template <int NB, bool TAIL, int GAP>
-__device__ __forceinline__ void mma_accumulate(uint32_t d, uint32_t a, uint64_t b, uint64_t bt, bool first) {
-    constexpr uint32_t id = idesc_bf16_f32(kTile, NB * 64, true);
-    constexpr uint32_t idt = idesc_bf16_f32(kTile, 16, true);
-#pragma unroll
-    for (int kk = 0; kk < kTile / 16; ++kk) {
-        const uint32_t ak = a + kk / (kCols / 16) * GAP + kk % (kCols / 16) * 8;
-        const uint32_t acc = (!first || kk > 0) ? 1u : 0u;
-        tc_mma_f16_ts(d, ak, b + ((kk * 2048) >> 4), id, acc);
-        if constexpr (TAIL) tc_mma_f16_ts(d + NB * 64, ak, bt + ((kk * 512) >> 4), idt, acc);
-    }
-}
-
-// x as the sum of three bf16 values (to ~2^-24 of x), two of them in one word.
-__device__ __forceinline__ void split3(float x, uint32_t& hi_mid, uint32_t& lo) {
-    const float a = __bfloat162float(__float2bfloat16_rn(x));
-    const float b = __bfloat162float(__float2bfloat16_rn(x - a));
-    hi_mid = pack_bf16x2(a, b);
-    lo = __bfloat16_as_ushort(__float2bfloat16_rn(x - a - b));
-}
-
-// One thread's part of an accumulator row (32-column chunks first, first +
-// step, ...) times `scale`: in fp32 to `part` if that is set, else in bf16 to the
-// tile in shared memory that TMA then stores (rows and columns past the tensor
-// are not written).  `none`: zeros instead, for a row without a visible pair; its
-// accumulator is 0, or NaN where the tile's other rows met an infinity.
-template <int NB, bool TAIL>
-__device__ __forceinline__ void store_row(uint32_t t, uint8_t* tile, int row, float* part, int hd, bool live, bool none, float scale,
-                                          int first, int step) {
-#pragma unroll 1
-    for (int c = first; c < (AttnTile<NB, TAIL>::HDP + 31) / 32; c += step) {
-        uint32_t r[32], w[16];
-        tmem_ld_32x32b_x32(t + c * 32, r);
-        tmem_wait_ld_r(r);
-        if (none) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) r[k] = 0;
-        }
-        if (part) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (live && c * 32 + 4 * k < hd)
-                    *reinterpret_cast<float4*>(part + c * 32 + 4 * k) =
-                        make_float4(__uint_as_float(r[4 * k]) * scale, __uint_as_float(r[4 * k + 1]) * scale,
-                                    __uint_as_float(r[4 * k + 2]) * scale, __uint_as_float(r[4 * k + 3]) * scale);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
-            put_row<NB, TAIL>(tile, row, c, w);
-        }
-    }
-}
 
 // Zeros to rows [0, n) x hd of a strided bf16 matrix, by the whole CTA.
 __device__ __forceinline__ void zero_out(__nv_bfloat16* out, int ld, int n, int hd) {
@@ -289,44 +81,6 @@ __device__ __forceinline__ void zero_out(float* out, int ld, int n, int hd) {
         reinterpret_cast<float4*>(out + static_cast<size_t>(i / c4) * ld)[i % c4] = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]));
-        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&y[i]));
-        t += u.x * v.x + u.y * v.y;
-    }
-    return t;
-}
-
-// The end of an issuing warp: on an abort, its MMAs in flight are waited for.
-template <typename Fail>
-__device__ __forceinline__ void end_issue(bool one, bool ok, uint32_t drain, const volatile int* abort_flag, const Fail& fail) {
-    if (one) {
-        if (!ok) fail();
-        if (*abort_flag) {
-            tc_commit(drain);
-            mbar_wait(drain, 0, nullptr);
-        }
-    }
-    __syncwarp();
-}
-
-// A raw score that no score makes up for: exp of it is 0, and times 0 it is 0.
-constexpr float kNothing = -1e30f;
-
-// Row `r` of a statistics operand.
-__device__ __forceinline__ void write_stat(uint4* stat, int r, float neg_l, float neg_d) {
-    uint32_t l01, l2, d01, d2;
-    split3(neg_l, l01, l2);
-    split3(neg_d, d01, d2);
-    const int x = (r >> 2) & 1;          // 32-byte swizzle: the row's two pieces change places
-    stat[2 * r + x] = make_uint4(l01, l2 | (d01 << 16), (d01 >> 16) | (d2 << 16), 0);
-    stat[2 * r + 1 - x] = make_uint4(0, 0, 0, 0);
-}
-
 // ------------------------------------------------------------------ dQ
 // TMEM: S [0, 128), dP [128, 256), dS [256, 320), dQ [384, 512).  Issue order
 // S_0 dP_0 | S_1 dP_1 dQ_0 | S_2 dP_2 dQ_1 | ...: S_{j+1} goes once S_j is read
@@ -334,7 +88,7 @@ __device__ __forceinline__ void write_stat(uint4* stat, int r, float neg_l, floa
 // so that they find their next operands ready.  Two warps issue, S and dP one, dQ
 // the other: each waits for its own barriers while the other's products run (a
 // tile at head dim 64: 0.74 us, against 0.84 with one).
-template <int NB, bool TAIL, bool PK>
+template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dq_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
     using P = BwdPlan<NB, TAIL, true>;
@@ -354,40 +108,24 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     // with a causal mask the last query tiles see the most keys: first
     const int qtiles = gridDim.x / g.splits_q, split = blockIdx.x % g.splits_q;
-    const int slot = qtiles - 1 - blockIdx.x / g.splits_q, h = blockIdx.y, b = blockIdx.z;
+    const int qt = qtiles - 1 - blockIdx.x / g.splits_q, h = blockIdx.y, b = blockIdx.z;
+    const int row0 = qt * kTile, off = g.nk - g.nq;
 
     pdl_wait();
-    int qt = slot, nq = g.nq, nk = g.nk, qlen, klen;      // of one sequence
-    int q0 = 0, k0 = 0;                                   // PK: its first rows
-    if constexpr (PK) {
-        const PackedTile p = packed_tile(g.q_lens, g.batch, g.nq, kTile, slot);
-        if (p.tile < 0) return;
-        qt = p.tile;
-        q0 = p.row0;
-        k0 = seq_start(g.k_lens, p.b, g.nk);
-        qlen = nq = p.n;
-        klen = nk = max(0, seq_start(g.k_lens, p.b + 1, g.nk) - k0);
-    } else {
-        qlen = seq_len(g.q_lens, b, nq);
-        klen = seq_len(g.k_lens, b, nk);
-    }
-    const int row0 = qt * kTile, off = nk - nq;
-    // the tile's first row in the matrices and in the row statistics
-    const size_t out0 = PK ? static_cast<size_t>(q0) + row0 : static_cast<size_t>(b) * nq + row0;
-    const size_t lse0 = PK ? static_cast<size_t>(h) * g.nq + q0 + row0 : (static_cast<size_t>(b) * g.heads + h) * nq + row0;
+    const int qlen = seq_len(g.q_lens, b, g.nq), klen = seq_len(g.k_lens, b, g.nk);
     const int last = min(row0 + kTile, qlen) - 1;
     const int all = last < row0 ? 0 : (key_end(last, off, g.causal_block, klen) + kTile - 1) / kTile;
     // key tiles [j0, j0 + n) are this CTA's
     const int per = (all + g.splits_q - 1) / g.splits_q, j0 = split * per, n = min(all, j0 + per) - j0;
-    uint4* stat = split ? nullptr : g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + slot) * (kStatBytes / 16);
-    __nv_bfloat16* dq0 = g.dQ + out0 * g.lddq + h * g.hd;
+    uint4* stat = split ? nullptr : g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16);
+    __nv_bfloat16* dq0 = g.dQ + (static_cast<size_t>(b) * g.nq + row0) * g.lddq + h * g.hd;
     const int ldp = g.heads * g.hd;
     float* part0 = g.splits_q == 1 ? nullptr
-                                   : g.part_q + (static_cast<size_t>(split) * gridDim.z * g.nq + out0) * ldp + h * g.hd;
+                                   : g.part_q + ((static_cast<size_t>(split) * gridDim.z + b) * g.nq + row0) * ldp + h * g.hd;
     if (n <= 0) {
         if (stat && threadIdx.x < kTile) write_stat(stat, threadIdx.x, kNothing, 0.f);
-        if (part0) zero_out(part0, ldp, min(kTile, nq - row0), g.hd);
-        else zero_out(dq0, g.lddq, min(kTile, nq - row0), g.hd);
+        if (part0) zero_out(part0, ldp, min(kTile, g.nq - row0), g.hd);
+        else zero_out(dq0, g.lddq, min(kTile, g.nq - row0), g.hd);
         return;
     }
 
@@ -406,12 +144,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         for (int u = 0; u < 8 / RP; ++u) {
             const int row = (warp - 4) * 8 + u * RP + lane / LP, c = lane % LP;
             const bool in = !one_tile && row0 + row < qlen && c < g.hd / 8;
-            const size_t r = out0 + row;
+            const size_t r = static_cast<size_t>(b) * g.nq + row0 + row;
             o[u] = in ? reinterpret_cast<const uint4*>(g.O + r * g.ldo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
             d[u] = in ? reinterpret_cast<const uint4*>(g.dO + r * g.lddo + h * g.hd)[c] : make_uint4(0, 0, 0, 0);
         }
-        const int i = (warp & 3) * 32 + lane;
-        if (row0 + i < qlen) l = g.lse[lse0 + i];
+        const int i = row0 + (warp & 3) * 32 + lane;
+        if (i < qlen) l = g.lse[(static_cast<size_t>(b) * g.heads + h) * g.nq + i];
     }
     if (threadIdx.x == 0) {
         bwd_init<P::SLOTS>(m, 1, 1);
@@ -419,8 +157,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         // this thread is also the one that loads: the first tiles need not wait
         // for the rest of the set-up
         mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
-        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, q0 + row0, b, m.a_full);
-        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, q0 + row0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.q, &maps.qt, h, row0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.d, &maps.dt, h, row0, b, m.a_full);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -443,8 +181,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     };
     // keys behind k_lens end inside the last tile: its K rows there become zero
     // before the MMAs see it (its loads complete on raw0 instead)
-    // (PK: the next sequence's rows)
-    const int fix = (PK || klen < nk) && klen < (j0 + n) * kTile ? klen - (j0 + n - 1) * kTile : kTile;
+    const int fix = klen < g.nk && klen < (j0 + n) * kTile ? klen - (j0 + n - 1) * kTile : kTile;
 
     if (warp == 0) {
         // ---------------- TMA: K and V
@@ -458,7 +195,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 const bool raw = fix < kTile && j == n - 1;
                 const uint32_t full = raw ? m.raw0 : m.full + 8 * k.s;
                 mbar_arrive_expect_tx(full, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R_OFF + k.s * P::TILE, &maps.k, &maps.kt, hk, k0 + (j0 + j) * kTile, b, full);
+                load_tile<NB, TAIL>(sb + P::R_OFF + k.s * P::TILE, &maps.k, &maps.kt, hk, (j0 + j) * kTile, b, full);
                 if (!raw) in.add(k);
                 if (!mbar_wait(m.empty + 8 * v.s, v.ph ^ 1, abort_flag)) {
                     ok = false;
@@ -466,7 +203,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                     break;
                 }
                 mbar_arrive_expect_tx(m.full + 8 * v.s, P::TILE);
-                load_tile<NB, TAIL>(sb + P::R_OFF + v.s * P::TILE, &maps.v, &maps.vt, hk, k0 + (j0 + j) * kTile, b, m.full + 8 * v.s);
+                load_tile<NB, TAIL>(sb + P::R_OFF + v.s * P::TILE, &maps.v, &maps.vt, hk, (j0 + j) * kTile, b, m.full + 8 * v.s);
                 in.add(v);
             }
         }
@@ -639,22 +376,17 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         } else {
             tc_fence_after();
             // the slots' tiles have all been read: the first one takes the result
-            store_row<NB, TAIL>(tl + 384, smem + P::R_OFF, row, part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < nq,
+            store_row<NB, TAIL>(tl + 384, smem + P::R_OFF, row, part0 ? part0 + static_cast<size_t>(row) * ldp : nullptr, g.hd, i < g.nq,
                                 end <= 0, g.scale, e, kGroups);
             if (!part0) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m.staged);
-                if (PK && nq - row0 < kTile) {
-                    if (warp_wait(m.staged, 0, abort_flag))
-                        copy_rows<NB, TAIL>(smem + P::R_OFF, dq0, g.lddq, nq - row0, 1, g.hd, threadIdx.x - 128, kThreadsB - 128);
-                    else if (lane == 0)
-                        fail();
-                } else if (warp == 4) {
+                if (warp == 4) {
                     ok = warp_wait(m.staged, 0, abort_flag);
                     if (lane == 0) {
                         if (ok) {
-                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gq, &maps.gqt, h, q0 + row0, b);
+                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gq, &maps.gqt, h, row0, b);
                             bulk_commit();
                             bulk_wait_all();
                         } else {
@@ -679,7 +411,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 // TMEM: S^T [0, 128), dP^T [128, 256), then dV, dK and, where they fit, P^T and
 // dS^T; else these take the places of S^T and dP^T, and then dV_i goes before
 // S_{i+1} and dK_i before dP_{i+1} in one order of issue.
-template <int NB, bool TAIL, bool PK>
+template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     dkv_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdArgs g) {
     using P = BwdPlan<NB, TAIL, false>;
@@ -698,9 +430,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         return;
     }
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int split = blockIdx.x % g.splits_k, hk = blockIdx.y, b = blockIdx.z;
-    int kt = blockIdx.x / g.splits_k;
-    int qtiles = PK ? packed_slots(g.nq, g.batch, kTile) : (g.nq + kTile - 1) / kTile;     // of a head's row statistics
+    const int kt = blockIdx.x / g.splits_k, split = blockIdx.x % g.splits_k, hk = blockIdx.y, b = blockIdx.z;
+    const int key0 = kt * kTile, off = g.nk - g.nq;
+    const int qtiles = (g.nq + kTile - 1) / kTile;
 
     // This grid starts while dq_kernel, whose every CTA has waited for what came
     // before, ends: all inputs are there, and only the row statistics, dq_kernel's
@@ -708,45 +440,26 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // for this grid has waited for dq_kernel too.  (In a graph, 256 tokens of 4 heads
     // of 64: 10.1 us for the two launches, 11.3 with the wait here; 2 x 16 heads of
     // 72, 1024 tokens: 48.8, 50.4 with it.)
-    int nq = g.nq, nk = g.nk, qlen, klen;                 // of one sequence
-    int q0 = 0, k0 = 0, slot0 = 0;                        // PK: its first rows and the slot of its first query tile
-    if constexpr (PK) {
-        const PackedTile p = packed_tile(g.k_lens, g.batch, g.nk, kTile, kt);
-        if (p.tile < 0) {
-            pdl_wait();
-            return;
-        }
-        kt = p.tile;
-        k0 = p.row0;
-        q0 = seq_start(g.q_lens, p.b, g.nq);
-        klen = nk = p.n;
-        qlen = nq = max(0, seq_start(g.q_lens, p.b + 1, g.nq) - q0);
-        slot0 = q0 / kTile + p.b;
-    } else {
-        qlen = seq_len(g.q_lens, b, nq);
-        klen = seq_len(g.k_lens, b, nk);
-    }
-    const int key0 = kt * kTile, off = nk - nq;
-    const size_t out0 = PK ? static_cast<size_t>(k0) + key0 : static_cast<size_t>(b) * nk + key0;
+    const int qlen = seq_len(g.q_lens, b, g.nq), klen = seq_len(g.k_lens, b, g.nk);
     // query tiles [t0, t1) of each of the group's heads, one after the other
     const int t0 = max(0, query_begin(key0, off, g.causal_block)) / kTile;
     const int t1 = key0 < klen ? (qlen + kTile - 1) / kTile : 0;
     const int per = max(0, t1 - t0), all = per * g.group;
     // of these `all` steps, [i0, i0 + n) are this CTA's
     const int share = (all + g.splits_k - 1) / g.splits_k, i0 = split * share, n = min(all, i0 + share) - i0;
-    __nv_bfloat16* dk0 = g.dK + out0 * g.lddk + hk * g.hd;
-    __nv_bfloat16* dv0 = g.dV + out0 * g.lddv + hk * g.hd;
+    __nv_bfloat16* dk0 = g.dK + (static_cast<size_t>(b) * g.nk + key0) * g.lddk + hk * g.hd;
+    __nv_bfloat16* dv0 = g.dV + (static_cast<size_t>(b) * g.nk + key0) * g.lddv + hk * g.hd;
     const int ldp = gridDim.y * g.hd;
-    const size_t part_at = (static_cast<size_t>(split) * gridDim.z * g.nk + out0) * ldp + hk * g.hd;
+    const size_t part_at = ((static_cast<size_t>(split) * gridDim.z + b) * g.nk + key0) * ldp + hk * g.hd;
     const bool parts = g.splits_k > 1;
     if (n <= 0) {
         pdl_wait();
         if (parts) {
-            zero_out(g.part_k + part_at, ldp, min(kTile, nk - key0), g.hd);
-            zero_out(g.part_v + part_at, ldp, min(kTile, nk - key0), g.hd);
+            zero_out(g.part_k + part_at, ldp, min(kTile, g.nk - key0), g.hd);
+            zero_out(g.part_v + part_at, ldp, min(kTile, g.nk - key0), g.hd);
         } else {
-            zero_out(dk0, g.lddk, min(kTile, nk - key0), g.hd);
-            zero_out(dv0, g.lddv, min(kTile, nk - key0), g.hd);
+            zero_out(dk0, g.lddk, min(kTile, g.nk - key0), g.hd);
+            zero_out(dv0, g.lddv, min(kTile, g.nk - key0), g.hd);
         }
         return;
     }
@@ -755,8 +468,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         bwd_init<P::SLOTS>(m, M::ISSUERS, M::ISSUERS);
         *abort_flag = 0;
         mbar_arrive_expect_tx(m.a_full, 2 * P::TILE);
-        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, k0 + key0, b, m.a_full);
-        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.v, &maps.vt, hk, k0 + key0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A0_OFF, &maps.k, &maps.kt, hk, key0, b, m.a_full);
+        load_tile<NB, TAIL>(sb + P::A1_OFF, &maps.v, &maps.vt, hk, key0, b, m.a_full);
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
         tma_prefetch_desc(&maps.v);
@@ -787,8 +500,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     };
     // queries behind q_lens end inside each head's last tile: its Q and dO rows
     // there become zero before the MMAs see it (loads complete on raw0, raw1)
-    // (PK: the next sequence's rows)
-    const int fix = (PK || qlen < nq) && qlen < t1 * kTile ? qlen - (t1 - 1) * kTile : kTile;
+    const int fix = qlen < g.nq && qlen < t1 * kTile ? qlen - (t1 - 1) * kTile : kTile;
 
     if (warp == 0) {
         // ---------------- TMA: Q with the row statistics, and dO
@@ -804,15 +516,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 ok = mbar_wait(m.empty + 8 * q.s, q.ph ^ 1, abort_flag);
                 if (ok) {
                     mbar_arrive_expect_tx(full0, P::TILE + kStatBytes);
-                    load_tile<NB, TAIL>(sb + P::R_OFF + q.s * P::TILE, &maps.q, &maps.qt, h, q0 + qt * kTile, b, full0);
+                    load_tile<NB, TAIL>(sb + P::R_OFF + q.s * P::TILE, &maps.q, &maps.qt, h, qt * kTile, b, full0);
                     if (i == 0) pdl_wait();
                     bulk_load(sb + P::STAT_OFF + i % P::STATS * kStatBytes,
-                              g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + slot0 + qt) * (kStatBytes / 16), kStatBytes, full0);
+                              g.stats + ((static_cast<size_t>(b) * g.heads + h) * qtiles + qt) * (kStatBytes / 16), kStatBytes, full0);
                     if (!raw) in.add(q);
                     ok = mbar_wait(m.empty + 8 * d.s, d.ph ^ 1, abort_flag);
                     if (ok) {
                         mbar_arrive_expect_tx(full1, P::TILE);
-                        load_tile<NB, TAIL>(sb + P::R_OFF + d.s * P::TILE, &maps.d, &maps.dt, h, q0 + qt * kTile, b, full1);
+                        load_tile<NB, TAIL>(sb + P::R_OFF + d.s * P::TILE, &maps.d, &maps.dt, h, qt * kTile, b, full1);
                         if (!raw) in.add(d);
                     } else if (raw) {
                         mbar_wait(m.raw0, raws & 1, nullptr);
@@ -1054,26 +766,18 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             // even groups bring dV, odd ones dK, into the first two slots
             const bool k = e & 1;
             float* part = parts ? (k ? g.part_k : g.part_v) + part_at + static_cast<size_t>(row) * ldp : nullptr;
-            store_row<NB, TAIL>(tl + (k ? M::DK_COL : M::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < nk,
+            store_row<NB, TAIL>(tl + (k ? M::DK_COL : M::DV_COL), smem + P::R_OFF + (k ? P::TILE : 0), row, part, g.hd, key < g.nk,
                                 begin >= qlen, k ? g.scale : 1.f, e >> 1, kGroups / 2);
             if (!parts) {
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(m.staged);
-                if (PK && nk - key0 < kTile) {
-                    if (warp_wait(m.staged, 0, abort_flag)) {
-                        copy_rows<NB, TAIL>(smem + P::R_OFF, dv0, g.lddv, nk - key0, 1, g.hd, threadIdx.x - 128, kThreadsB - 128);
-                        copy_rows<NB, TAIL>(smem + P::R_OFF + P::TILE, dk0, g.lddk, nk - key0, 1, g.hd, threadIdx.x - 128,
-                                            kThreadsB - 128);
-                    } else if (lane == 0) {
-                        fail();
-                    }
-                } else if (warp == 4) {
+                if (warp == 4) {
                     ok = warp_wait(m.staged, 0, abort_flag);
                     if (lane == 0) {
                         if (ok) {
-                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gv, &maps.gvt, hk, k0 + key0, b);
-                            store_tile<NB, TAIL>(sb + P::R_OFF + P::TILE, &maps.gk, &maps.gkt, hk, k0 + key0, b);
+                            store_tile<NB, TAIL>(sb + P::R_OFF, &maps.gv, &maps.gvt, hk, key0, b);
+                            store_tile<NB, TAIL>(sb + P::R_OFF + P::TILE, &maps.gk, &maps.gkt, hk, key0, b);
                             bulk_commit();
                             bulk_wait_all();
                         } else {
@@ -1101,8 +805,6 @@ struct JoinOne {
     __nv_bfloat16* out;
     int splits, ld, c8;          // c8: pieces of 8 columns a row
     long long rows;
-    const int* starts;           // packed: rows of no sequence stay as they are
-    int batch;
 };
 struct JoinArgs {
     JoinOne one[3];
@@ -1120,8 +822,6 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ J
             i -= n;
             continue;
         }
-        const long long row = i / j.c8;
-        if (j.starts && (row < __ldcg(j.starts) || row >= __ldcg(j.starts + j.batch))) return;
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
         const float4* p = reinterpret_cast<const float4*>(j.part) + 2 * i;
 #pragma unroll 4
@@ -1130,6 +830,7 @@ __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ J
             x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
             y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
         }
+        const long long row = i / j.c8;
         reinterpret_cast<uint4*>(j.out + row * j.ld)[i - row * j.c8] =
             make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w), pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
         return;
@@ -1147,11 +848,9 @@ struct BwdSplit {
     size_t part_q, part_k, part_v, total;      // byte offsets
 };
 
-// qt, kt: query and key tiles of a sequence (packed: of a mean one); tiles_q, tiles_k: of
-// all; rows_q, rows_k: of all.
-BwdSplit bwd_split(int heads, int kv_heads, int head_dim, bool causal, long long qt, long long kt, long long tiles_q,
-                   long long tiles_k, size_t rows_q, size_t rows_k) {
-    const long long nq = tiles_q * heads, nk = tiles_k * kv_heads, steps = qt * (heads / kv_heads);
+BwdSplit bwd_split(const dlo_attn& a) {
+    const long long qt = (a.nq + kTile - 1) / kTile, kt = (a.nk + kTile - 1) / kTile, group = a.heads / a.kv_heads;
+    const long long nq = qt * a.heads * a.batch, nk = kt * a.kv_heads * a.batch, steps = qt * group;
     const auto fill = [](long long ctas, long long work) {
         long long s = kGb300Sms / ctas;
         if (s > work / 4) s = work / 4;
@@ -1159,7 +858,7 @@ BwdSplit bwd_split(int heads, int kv_heads, int head_dim, bool causal, long long
     };
     BwdSplit b;
     long long sq = fill(nq, kt), sk = fill(nk, steps);
-    if (causal) {
+    if (a.causal_block > 0) {
         // about half of all steps are done
         const long long mean = nk * steps / 2 / kGb300Sms + 1;
         long long s = (steps + mean - 1) / mean;
@@ -1168,139 +867,99 @@ BwdSplit bwd_split(int heads, int kv_heads, int head_dim, bool causal, long long
     }
     b.q = static_cast<int>(sq);
     b.k = static_cast<int>(sk);
-    const size_t rq = rows_q * heads * head_dim * sizeof(float), rk = rows_k * kv_heads * head_dim * sizeof(float);
-    b.part_q = static_cast<size_t>(tiles_q) * heads * kStatBytes;
+    const size_t rq = static_cast<size_t>(a.batch) * a.nq * a.heads * a.head_dim * sizeof(float);
+    const size_t rk = static_cast<size_t>(a.batch) * a.nk * a.kv_heads * a.head_dim * sizeof(float);
+    b.part_q = static_cast<size_t>(a.batch) * a.heads * qt * kStatBytes;
     b.part_k = b.part_q + (b.q > 1 ? b.q * rq : 0);
     b.part_v = b.part_k + (b.k > 1 ? b.k * rk : 0);
     b.total = b.part_v + (b.k > 1 ? b.k * rk : 0);
     return b;
 }
 
-BwdSplit bwd_split(const dlo_attn& a) {
-    const long long qt = (a.nq + kTile - 1) / kTile, kt = (a.nk + kTile - 1) / kTile;
-    return bwd_split(a.heads, a.kv_heads, a.head_dim, a.causal_block > 0, qt, kt, qt * a.batch, kt * a.batch,
-                     static_cast<size_t>(a.batch) * a.nq, static_cast<size_t>(a.batch) * a.nk);
-}
-
-BwdSplit bwd_split(const dlo_attn_packed& a) {
-    return bwd_split(a.heads, a.kv_heads, a.head_dim, a.causal_block > 0, (a.rows_q / a.batch + kTile) / kTile,
-                     (a.rows_k / a.batch + kTile) / kTile, packed_slots(a.rows_q, a.batch, kTile),
-                     packed_slots(a.rows_k, a.batch, kTile), a.rows_q, a.rows_k);
-}
-
-template <int NB, bool TAIL, bool PACKED>
+template <int NB, bool TAIL>
 cudaError_t run_bwd(const BwdMaps& maps, const BwdArgs& g, int batch, int kv_heads, cudaStream_t s,
                     unsigned long long* launches) {
     using PQ = BwdPlan<NB, TAIL, true>;
     using PK = BwdPlan<NB, TAIL, false>;
-    constexpr auto dq = dq_kernel<NB, TAIL, PACKED>;
-    constexpr auto dkv = dkv_kernel<NB, TAIL, PACKED>;
     static unsigned long long set[2] = {0, 0};
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(dq), PQ::BYTES, &set[0]); e != cudaSuccess) return e;
-    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(dkv), PK::BYTES, &set[1]); e != cudaSuccess) return e;
-    const int tq = PACKED ? packed_slots(g.nq, g.batch, kTile) : (g.nq + kTile - 1) / kTile;
-    const int tk = PACKED ? packed_slots(g.nk, g.batch, kTile) : (g.nk + kTile - 1) / kTile;
-    cudaError_t e = launch_k(dq, dim3(tq * g.splits_q, g.heads, batch), kThreadsB, PQ::BYTES, s, maps, g);
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dq_kernel<NB, TAIL>), PQ::BYTES, &set[0]); e != cudaSuccess) return e;
+    if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(&dkv_kernel<NB, TAIL>), PK::BYTES, &set[1]); e != cudaSuccess) return e;
+    cudaError_t e = launch_k(dq_kernel<NB, TAIL>, dim3((g.nq + kTile - 1) / kTile * g.splits_q, g.heads, batch), kThreadsB, PQ::BYTES, s, maps, g);
     ++*launches;
     if (e != cudaSuccess) return e;
-    e = launch_k(dkv, dim3(tk * g.splits_k, kv_heads, batch), kThreadsB, PK::BYTES, s, maps, g);
-    ++*launches;
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-struct BwdPointers {
-    const void *Q, *K, *V, *O;
-    const float* lse;
-    const void* dO;
-    void *dQ, *dK, *dV, *ws;
-    int* err;
-};
-
-// Both forms, whose descriptions name the same things: `batch` sequences of nq and nk
-// rows, or (PACKED) one of all rows.
-template <bool PACKED, typename Attn>
-cudaError_t launch_bwd(const Attn& a, int batch, int nq, int nk, const int* q_seq, const int* k_seq, const BwdPointers& p,
-                       cudaStream_t s, unsigned long long* launches) {
-    const int hd = a.head_dim;
-    BwdArgs g = {};
-    g.q_lens = q_seq;
-    g.k_lens = k_seq;
-    g.nq = nq;
-    g.nk = nk;
-    g.batch = a.batch;
-    g.hd = hd;
-    g.heads = a.heads;
-    g.group = a.heads / a.kv_heads;
-    g.causal_block = a.causal_block < nk ? a.causal_block : nk;
-    g.scale = 1.f / sqrtf(static_cast<float>(hd));
-    g.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
-    g.O = static_cast<const __nv_bfloat16*>(p.O);
-    g.dO = static_cast<const __nv_bfloat16*>(p.dO);
-    g.lse = p.lse;
-    g.stats = static_cast<uint4*>(p.ws);
-    const BwdSplit split = bwd_split(a);
-    uint8_t* base = static_cast<uint8_t*>(p.ws);
-    g.splits_q = split.q;
-    g.splits_k = split.k;
-    g.part_q = reinterpret_cast<float*>(base + split.part_q);
-    g.part_k = reinterpret_cast<float*>(base + split.part_k);
-    g.part_v = reinterpret_cast<float*>(base + split.part_v);
-    g.dQ = static_cast<__nv_bfloat16*>(p.dQ);
-    g.dK = static_cast<__nv_bfloat16*>(p.dK);
-    g.dV = static_cast<__nv_bfloat16*>(p.dV);
-    g.ldo = a.ldo;
-    g.lddo = a.lddo;
-    g.lddq = a.lddq;
-    g.lddk = a.lddk;
-    g.lddv = a.lddv;
-    g.err = p.err;
-    BwdMaps m;
-    const CUtensorMapSwizzle w128 = CU_TENSOR_MAP_SWIZZLE_128B, w32 = CU_TENSOR_MAP_SWIZZLE_32B;
-    const bool tail = hd > 64 && hd <= 80;
-    auto map = [&](CUtensorMap* main, CUtensorMap* tl, const void* q, int rows, int heads, int ld) {
-        if (!make_map4(main, q, batch, rows, heads, hd, ld, 64, w128)) return false;
-        if (tail) return make_map4(tl, q, batch, rows, heads, hd, ld, 16, w32);
-        *tl = *main;
-        return true;
-    };
-    if (!map(&m.q, &m.qt, p.Q, nq, a.heads, a.ldq) || !map(&m.k, &m.kt, p.K, nk, a.kv_heads, a.ldk) ||
-        !map(&m.v, &m.vt, p.V, nk, a.kv_heads, a.ldv) || !map(&m.d, &m.dt, p.dO, nq, a.heads, a.lddo) ||
-        !map(&m.gq, &m.gqt, p.dQ, nq, a.heads, a.lddq) || !map(&m.gk, &m.gkt, p.dK, nk, a.kv_heads, a.lddk) ||
-        !map(&m.gv, &m.gvt, p.dV, nk, a.kv_heads, a.lddv))
-        return cudaErrorInvalidValue;
-    cudaError_t e = hd <= 64 ? run_bwd<1, false, PACKED>(m, g, batch, a.kv_heads, s, launches)
-                    : tail   ? run_bwd<1, true, PACKED>(m, g, batch, a.kv_heads, s, launches)
-                             : run_bwd<2, false, PACKED>(m, g, batch, a.kv_heads, s, launches);
-    if (e != cudaSuccess || (split.q == 1 && split.k == 1)) return e;
-    const long long rq = static_cast<long long>(batch) * nq, rk = static_cast<long long>(batch) * nk;
-    const int cq = a.heads * hd / 8, ck = a.kv_heads * hd / 8;
-    const int *sq = PACKED ? q_seq : nullptr, *sk = PACKED ? k_seq : nullptr;
-    const JoinArgs j = {{{g.part_q, g.dQ, split.q, a.lddq, cq, split.q > 1 ? rq : 0, sq, a.batch},
-                         {g.part_k, g.dK, split.k, a.lddk, ck, split.k > 1 ? rk : 0, sk, a.batch},
-                         {g.part_v, g.dV, split.k, a.lddv, ck, split.k > 1 ? rk : 0, sk, a.batch}}};
-    const long long n = j.one[0].rows * cq + 2 * j.one[1].rows * ck;
-    e = launch_k(bwd_join_kernel, static_cast<unsigned>((n + 255) / 256), 256, 0, s, j);
+    e = launch_k(dkv_kernel<NB, TAIL>, dim3((g.nk + kTile - 1) / kTile * g.splits_k, kv_heads, batch), kThreadsB, PK::BYTES, s, maps, g);
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-size_t attention_bwd_workspace(const dlo_attn& a) { return bwd_split(a).total; }
-
-size_t attention_packed_bwd_workspace(const dlo_attn_packed& a) { return bwd_split(a).total; }
+size_t attention_bwd_workspace(const dlo_attn& a) {
+    return bwd_split(a).total;
+}
 
 cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K, const void* V, const void* O,
                                  const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
                                  cudaStream_t s, unsigned long long* launches) {
-    return launch_bwd<false>(a, a.batch, a.nq, a.nk, a.q_lens, a.k_lens, {Q, K, V, O, lse, dO, dQ, dK, dV, ws, err}, s, launches);
-}
-
-cudaError_t launch_attention_packed_bwd(const dlo_attn_packed& a, const void* Q, const void* K, const void* V, const void* O,
-                                        const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
-                                        cudaStream_t s, unsigned long long* launches) {
-    return launch_bwd<true>(a, 1, a.rows_q, a.rows_k, a.q_starts, a.k_starts, {Q, K, V, O, lse, dO, dQ, dK, dV, ws, err}, s,
-                            launches);
+    const int hd = a.head_dim;
+    BwdArgs g = {};
+    g.q_lens = a.q_lens;
+    g.k_lens = a.k_lens;
+    g.nq = a.nq;
+    g.nk = a.nk;
+    g.hd = hd;
+    g.heads = a.heads;
+    g.group = a.heads / a.kv_heads;
+    g.causal_block = a.causal_block < a.nk ? a.causal_block : a.nk;
+    g.scale = 1.f / sqrtf(static_cast<float>(hd));
+    g.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
+    g.O = static_cast<const __nv_bfloat16*>(O);
+    g.dO = static_cast<const __nv_bfloat16*>(dO);
+    g.lse = lse;
+    g.stats = static_cast<uint4*>(ws);
+    const BwdSplit split = bwd_split(a);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    g.splits_q = split.q;
+    g.splits_k = split.k;
+    g.part_q = reinterpret_cast<float*>(base + split.part_q);
+    g.part_k = reinterpret_cast<float*>(base + split.part_k);
+    g.part_v = reinterpret_cast<float*>(base + split.part_v);
+    g.dQ = static_cast<__nv_bfloat16*>(dQ);
+    g.dK = static_cast<__nv_bfloat16*>(dK);
+    g.dV = static_cast<__nv_bfloat16*>(dV);
+    g.ldo = a.ldo;
+    g.lddo = a.lddo;
+    g.lddq = a.lddq;
+    g.lddk = a.lddk;
+    g.lddv = a.lddv;
+    g.err = err;
+    BwdMaps m;
+    const CUtensorMapSwizzle w128 = CU_TENSOR_MAP_SWIZZLE_128B, w32 = CU_TENSOR_MAP_SWIZZLE_32B;
+    const bool tail = hd > 64 && hd <= 80;
+    auto map = [&](CUtensorMap* main, CUtensorMap* tl, const void* p, int rows, int heads, int ld) {
+        if (!make_map4(main, p, a.batch, rows, heads, hd, ld, 64, w128)) return false;
+        if (tail) return make_map4(tl, p, a.batch, rows, heads, hd, ld, 16, w32);
+        *tl = *main;
+        return true;
+    };
+    if (!map(&m.q, &m.qt, Q, a.nq, a.heads, a.ldq) || !map(&m.k, &m.kt, K, a.nk, a.kv_heads, a.ldk) ||
+        !map(&m.v, &m.vt, V, a.nk, a.kv_heads, a.ldv) || !map(&m.d, &m.dt, dO, a.nq, a.heads, a.lddo) ||
+        !map(&m.gq, &m.gqt, dQ, a.nq, a.heads, a.lddq) || !map(&m.gk, &m.gkt, dK, a.nk, a.kv_heads, a.lddk) ||
+        !map(&m.gv, &m.gvt, dV, a.nk, a.kv_heads, a.lddv))
+        return cudaErrorInvalidValue;
+    cudaError_t e = hd <= 64 ? run_bwd<1, false>(m, g, a.batch, a.kv_heads, s, launches)
+                    : tail   ? run_bwd<1, true>(m, g, a.batch, a.kv_heads, s, launches)
+                             : run_bwd<2, false>(m, g, a.batch, a.kv_heads, s, launches);
+    if (e != cudaSuccess || (split.q == 1 && split.k == 1)) return e;
+    const long long rq = static_cast<long long>(a.batch) * a.nq, rk = static_cast<long long>(a.batch) * a.nk;
+    const int cq = a.heads * hd / 8, ck = a.kv_heads * hd / 8;
+    const JoinArgs j = {{{g.part_q, g.dQ, split.q, a.lddq, cq, split.q > 1 ? rq : 0},
+                         {g.part_k, g.dK, split.k, a.lddk, ck, split.k > 1 ? rk : 0},
+                         {g.part_v, g.dV, split.k, a.lddv, ck, split.k > 1 ? rk : 0}}};
+    const long long n = j.one[0].rows * cq + 2 * j.one[1].rows * ck;
+    e = launch_k(bwd_join_kernel, static_cast<unsigned>((n + 255) / 256), 256, 0, s, j);
+    ++*launches;
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace dlo

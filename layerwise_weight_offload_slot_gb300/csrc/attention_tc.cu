@@ -80,37 +80,27 @@ struct AttnPlan {
     static_assert(!DUO || (NB == 1 && 2 * (USED + 1024) <= 228 * 1024), "DUO: two CTAs per SM");
 };
 
-// What a launch computes.
-//  kPlain    the blocks' own attention: every key, O alone
-//  kTrain    masks, shared key/value heads, row statistics, and a grid that may
-//            split the keys (partial results, joined by a second launch)
-//  kPacked   kTrain over packed sequences (packed_tile): a CTA's rows, keys and
-//            mask are those of its sequence, and it writes no row of another
-enum { kPlain, kTrain, kPacked };
-
+// The training form (TR): masks, shared key/value heads, row statistics, and a
+// grid that may split the keys (partial results, joined by a second launch).
 struct AttnTrain {
-    float* lse;                 // [batch, heads, nq]; kPacked [heads, rows]
-    const int *q_lens, *k_lens; // kPacked: q_starts, k_starts
+    float* lse;                 // [batch, heads, nq]
+    const int *q_lens, *k_lens;
     int causal_block, group, splits;
-    int gh;                     // query heads of a group that share a tile: row r is head r % gh of query r / gh
-    float *po, *pl;             // splits > 1: [splits][rows of lse][hd] and [..][rows]
-    int batch;                  // kPacked
+    int lg;                     // 2^lg query heads of a group share a tile: row r is head r % 2^lg of query r >> lg
+    float *po, *pl;             // splits > 1: [splits][batch][heads][nq][hd] and [..][nq]
 };
 
 struct AttnMaps {
     CUtensorMap q, k, v;        // 64-column boxes, 128-byte swizzle
     CUtensorMap qt, kt, vt;     // 16-column tail boxes, 32-byte swizzle
-    CUtensorMap o, ot;          // kTrain, kPacked: the output, stored by TMA
+    CUtensorMap o, ot;          // TR: the output, stored by TMA
 };
 
-template <int NB, bool TAIL, bool DUO, int FORM>
+template <int NB, bool TAIL, bool DUO, bool TR>
 __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     attn_tc_kernel(const __grid_constant__ AttnMaps maps, __nv_bfloat16* __restrict__ O, int hd,
-                   int rows_q, int rows_k, int ldo, float scale_log2, int* err, const AttnTrain tr) {
+                   int nq, int nk, int ldo, float scale_log2, int* err, const AttnTrain tr) {
     using P = AttnPlan<NB, TAIL, DUO>;
-    constexpr bool TR = FORM != kPlain, PK = FORM == kPacked;
-    int nq = rows_q, nk = rows_k;      // of one sequence
-    int q0 = 0, k0 = 0;                // PK: its first rows
     constexpr int HDP = P::HDP;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -130,38 +120,19 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     const int b = blockIdx.z;
     int h = blockIdx.y, qt = blockIdx.x, ntiles = (nk + TK - 1) / TK;
     int t0 = 0, hk = h, qlen = nq, klen = nk, split = 0;   // TR: first key tile, key/value head, valid rows
-    int nh = gridDim.y, tq = TQ, gh = 1;                   // TR: query heads, queries per tile, heads per tile
-    // TR: rows of the statistics and of O
-    const auto stat_row = [&](int head, int i) -> size_t {
-        return PK ? static_cast<size_t>(head) * rows_q + q0 + i : (static_cast<size_t>(b) * nh + head) * nq + i;
-    };
-    const auto out_row = [&](int i) -> size_t { return PK ? static_cast<size_t>(q0) + i : static_cast<size_t>(b) * nq + i; };
+    int nh = gridDim.y, tq = TQ;                           // TR: query heads, queries per tile
     if constexpr (TR) {
         pdl_wait();             // the lengths may come from the predecessor
+        const int off = nk - nq;
         split = qt % tr.splits;
         // with a causal mask the last query tiles have the most keys: first
         qt = gridDim.x / tr.splits - 1 - qt / tr.splits;
-        gh = tr.gh;
-        h *= gh;                // the first of the tile's heads
-        nh *= gh;
-        tq /= gh;
+        h <<= tr.lg;            // the first of the tile's heads
+        nh <<= tr.lg;
+        tq >>= tr.lg;
         hk = h / tr.group;
-        if constexpr (PK) {
-            const PackedTile p = packed_tile(tr.q_lens, tr.batch, rows_q, tq, qt);
-            if (p.tile < 0) {
-                pdl_launch_dependents();
-                return;
-            }
-            qt = p.tile;
-            q0 = p.row0;
-            k0 = seq_start(tr.k_lens, p.b, rows_k);
-            qlen = nq = p.n;
-            klen = nk = max(0, seq_start(tr.k_lens, p.b + 1, rows_k) - k0);
-        } else {
-            qlen = seq_len(tr.q_lens, b, nq);
-            klen = seq_len(tr.k_lens, b, nk);
-        }
-        const int off = nk - nq;
+        qlen = seq_len(tr.q_lens, b, nq);
+        klen = seq_len(tr.k_lens, b, nk);
         const int last = min(qt * tq + tq, qlen) - 1;
         ntiles = last < qt * tq ? 0 : (key_end(last, off, tr.causal_block, klen) + TK - 1) / TK;
         if (tr.splits > 1) {
@@ -171,14 +142,16 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         }
         if (ntiles <= 0) {      // no key for any of the rows
             pdl_launch_dependents();
-            float* lse = tr.splits > 1 ? tr.pl + static_cast<size_t>(split) * gridDim.z * nh * rows_q : tr.lse;
-            const int rows = min(nq - qt * tq, tq) * gh;
-            for (int r = threadIdx.x; r < rows; r += kThreadsA) lse[stat_row(h + r % gh, qt * tq + r / gh)] = -INFINITY;
+            float* lse = tr.splits > 1 ? tr.pl + static_cast<size_t>(split) * gridDim.z * nh * nq : tr.lse;
+            const int rows = min(nq - qt * tq, tq) << tr.lg;
+            for (int r = threadIdx.x; r < rows; r += kThreadsA)
+                lse[(static_cast<size_t>(b) * nh + h + (r & ((1 << tr.lg) - 1))) * nq + qt * tq + (r >> tr.lg)] = -INFINITY;
             if (tr.splits == 1) {
                 const int c8 = hd / 8;
                 for (int i = threadIdx.x; i < rows * c8; i += kThreadsA) {
                     const int r = i / c8;
-                    reinterpret_cast<uint4*>(O + out_row(qt * tq + r / gh) * ldo + (h + r % gh) * hd)[i % c8] = make_uint4(0, 0, 0, 0);
+                    reinterpret_cast<uint4*>(O + (static_cast<size_t>(b) * nq + qt * tq + (r >> tr.lg)) * ldo +
+                                             (h + (r & ((1 << tr.lg) - 1))) * hd)[i % c8] = make_uint4(0, 0, 0, 0);
                 }
             }
             return;
@@ -203,8 +176,8 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         *abort_flag = 0;
         fence_mbar_init();
         if constexpr (TR) {     // this thread is the one that loads, and has waited for the predecessor
-            mbar_arrive_expect_tx(q_full, P::TILE / TQ * (tq * gh));      // with 128 % gh != 0 the last rows stay empty
-            load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, q0 + qt * tq, b, q_full);
+            mbar_arrive_expect_tx(q_full, P::TILE);
+            load_tile<NB, TAIL>(sb + P::Q_OFF, &maps.q, &maps.qt, h, qt * tq, b, q_full);
         }
         tma_prefetch_desc(&maps.q);
         tma_prefetch_desc(&maps.k);
@@ -228,8 +201,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
 
     // TR: keys behind k_lens end inside the last tile; their V rows become zero
     // before the MMAs see that tile (its loads complete on `raw` instead)
-    // (PK: the next sequence's rows)
-    const int fix = TR && (PK || klen < nk) && klen < (t0 + ntiles) * TK ? klen - (t0 + ntiles - 1) * TK : TK;
+    const int fix = TR && klen < nk && klen < (t0 + ntiles) * TK ? klen - (t0 + ntiles - 1) * TK : TK;
     if (warp == 0) {
         // ---------------- TMA producer
         bool ok = true;
@@ -253,8 +225,8 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
                 const bool raw_tile = TR && fix < TK && j == ntiles - 1;
                 const uint32_t full = raw_tile ? raw : kv_full + 8 * st;
                 mbar_arrive_expect_tx(full, 2 * P::TILE);
-                load_tile<NB, TAIL>(sb + P::K_OFF + st * P::TILE, &maps.k, &maps.kt, hk, k0 + (t0 + j) * TK, b, full);
-                load_tile<NB, TAIL>(sb + P::V_OFF + st * P::TILE, &maps.v, &maps.vt, hk, k0 + (t0 + j) * TK, b, full);
+                load_tile<NB, TAIL>(sb + P::K_OFF + st * P::TILE, &maps.k, &maps.kt, hk, (t0 + j) * TK, b, full);
+                load_tile<NB, TAIL>(sb + P::V_OFF + st * P::TILE, &maps.v, &maps.vt, hk, (t0 + j) * TK, b, full);
                 if (raw_tile) break;
                 issued |= 1u << st;
                 par = (par & ~(1u << st)) | (ph << st);
@@ -368,7 +340,7 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
         bool ok = true;
         int row_end = nk;         // one past the last key of this row
         if constexpr (TR) {
-            const int i = qt * tq + row / gh;
+            const int i = qt * tq + (row >> tr.lg);
             row_end = i < qlen ? key_end(i, nk - nq, tr.causal_block, klen) : 0;
         }
         for (int j = 0; j < ntiles; ++j) {
@@ -469,24 +441,23 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
             // where the other rows' keys hold an infinite V
             const bool none = TR && l == 0.f;
             const float inv = none ? 0.f : 1.f / l;
-            int grow = qt * tq + (TR ? row / gh : row);
+            const int grow = qt * tq + (TR ? row >> tr.lg : row);
             const int h0 = h;
+            if constexpr (TR) h += row & ((1 << tr.lg) - 1);
             float* prow = nullptr;
             if constexpr (TR) {
-                h += row % gh;
-                if (row >= tq * gh) grow = nq;      // a row without a query
                 // natural logarithm of the sum of exp(scores)
                 const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * 0.6931471805599453f;
-                const size_t r = stat_row(h, grow);
+                const size_t r = (static_cast<size_t>(b) * nh + h) * nq + grow;
                 if (tr.splits > 1) {
-                    const size_t p = static_cast<size_t>(split) * gridDim.z * nh * rows_q + r;
+                    const size_t p = static_cast<size_t>(split) * gridDim.z * nh * nq + r;
                     prow = tr.po + p * hd;
                     if (grow < nq) tr.pl[p] = lse;
                 } else if (grow < nq) {
                     tr.lse[r] = lse;
                 }
             }
-            __nv_bfloat16* orow = O + out_row(grow) * ldo + h * hd;
+            __nv_bfloat16* orow = O + (static_cast<size_t>(b) * nq + grow) * ldo + h * hd;
 #pragma unroll 1
             for (int c = 0; c < (HDP + 31) / 32; ++c) {
                 uint32_t r[32];
@@ -527,16 +498,9 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(staged);
-                    const int rows = min(nq - qt * tq, tq);
-                    if (PK && rows < tq) {
-                        if (warp_wait(staged, 0, abort_flag))
-                            copy_rows<NB, TAIL>(smem + P::Q_OFF, O + out_row(qt * tq) * ldo + h0 * hd, ldo, rows * gh, gh, hd,
-                                                threadIdx.x - 64, kThreadsA - 64);
-                        else if (lane == 0)
-                            fail();
-                    } else if (warp == 2 && warp_wait(staged, 0, abort_flag)) {
+                    if (warp == 2 && warp_wait(staged, 0, abort_flag)) {
                         if (lane == 0) {
-                            store_tile<NB, TAIL>(sb + P::Q_OFF, &maps.o, &maps.ot, h0, q0 + qt * tq, b);
+                            store_tile<NB, TAIL>(sb + P::Q_OFF, &maps.o, &maps.ot, h0, qt * tq, b);
                             bulk_commit();
                             bulk_wait_all();
                         }
@@ -557,19 +521,18 @@ __global__ void __launch_bounds__(kThreadsA, DUO ? 2 : 1)
     }
 }
 
-template <int NB, bool TAIL, bool DUO, int FORM = kPlain>
+template <int NB, bool TAIL, bool DUO, bool TR = false>
 cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int batch, int heads,
                    int hd, int nq, int nk, int ldq, int ldk, int ldv, int ldo, int* err,
-                   cudaStream_t s, unsigned long long* launches, const AttnTrain& tr = AttnTrain{nullptr, nullptr, nullptr, 0, 1, 1, 1, nullptr, nullptr, 0}) {
+                   cudaStream_t s, unsigned long long* launches, const AttnTrain& tr = AttnTrain{nullptr, nullptr, nullptr, 0, 1, 1, 0, nullptr, nullptr}) {
     using P = AttnPlan<NB, TAIL, DUO>;
-    constexpr bool TR = FORM != kPlain;
     static_assert(P::BYTES <= 227 * 1024, "attention shared memory plan exceeds 227 KB");
-    const void* kernel = reinterpret_cast<const void*>(&attn_tc_kernel<NB, TAIL, DUO, FORM>);
+    const void* kernel = reinterpret_cast<const void*>(&attn_tc_kernel<NB, TAIL, DUO, TR>);
     static unsigned long long attr = 0;
     if (cudaError_t e = allow_smem(kernel, P::BYTES, &attr); e != cudaSuccess) return e;
     AttnMaps maps;
     const CUtensorMapSwizzle w128 = CU_TENSOR_MAP_SWIZZLE_128B, w32 = CU_TENSOR_MAP_SWIZZLE_32B;
-    const int qh = tr.gh;
+    const int qh = 1 << tr.lg;
     if (!make_map4(&maps.q, Q, batch, nq, heads, hd, ldq, 64, w128, qh) ||
         !make_map4(&maps.k, K, batch, nk, heads / tr.group, hd, ldk, 64, w128) ||
         !make_map4(&maps.v, V, batch, nk, heads / tr.group, hd, ldv, 64, w128))
@@ -592,9 +555,9 @@ cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int bat
             return cudaErrorInvalidValue;
     }
     const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hd));
-    const int tq = TQ / tr.gh;
-    dim3 grid((FORM == kPacked ? packed_slots(nq, tr.batch, tq) : (nq + tq - 1) / tq) * tr.splits, heads / tr.gh, batch);
-    cudaError_t le_ = launch_k(attn_tc_kernel<NB, TAIL, DUO, FORM>, grid, kThreadsA, P::BYTES, s, maps, static_cast<__nv_bfloat16*>(O), hd, nq, nk, ldo, scale_log2, err, tr);
+    const int tq = TQ >> tr.lg;
+    dim3 grid((nq + tq - 1) / tq * tr.splits, heads >> tr.lg, batch);
+    cudaError_t le_ = launch_k(attn_tc_kernel<NB, TAIL, DUO, TR>, grid, kThreadsA, P::BYTES, s, maps, static_cast<__nv_bfloat16*>(O), hd, nq, nk, ldo, scale_log2, err, tr);
     ++*launches;
     return le_ != cudaSuccess ? le_ : cudaGetLastError();
 }
@@ -638,15 +601,12 @@ namespace {
 __global__ void __launch_bounds__(256) attn_join_kernel(const float* __restrict__ po, const float* __restrict__ pl,
                                                         int splits, size_t rows, int nq, int heads, int hd,
                                                         __nv_bfloat16* __restrict__ O, int ldo,
-                                                        float* __restrict__ lse, const int* starts, int batch) {
+                                                        float* __restrict__ lse) {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
     const size_t r = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;     // (b, h, i)
     if (r >= rows) return;
-    const size_t bh = r / nq, i = r - bh * nq, b = bh / heads, h = bh - b * heads;
-    // packed (b = 0): rows of no sequence stay as they are
-    if (starts && (static_cast<int>(i) < __ldcg(starts) || static_cast<int>(i) >= __ldcg(starts + batch))) return;
     // lane p holds the weights of parts p and p + 32 (splits <= 64)
     const float l0 = lane < splits ? pl[lane * rows + r] : -INFINITY;
     const float l1 = lane + 32 < splits ? pl[(lane + 32) * rows + r] : -INFINITY;
@@ -669,6 +629,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const float* __restrict_
         }
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
+    const size_t bh = r / nq, i = r - bh * nq, b = bh / heads, h = bh - b * heads;
     if (4 * lane < hd)
         reinterpret_cast<uint2*>(O + (b * nq + i) * ldo + h * hd)[lane] =
             make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
@@ -715,13 +676,13 @@ cudaError_t launch_attention_fwd(const dlo_attn& a, const void* Q, const void* K
     const size_t rows = static_cast<size_t>(a.batch) * a.heads * a.nq;
     const FwdPlan plan = attn_fwd_plan(a);
     AttnTrain tr = {lse, a.q_lens, a.k_lens, a.causal_block < a.nk ? a.causal_block : a.nk, a.heads / a.kv_heads,
-                    plan.splits, 1 << plan.lg, static_cast<float*>(ws), nullptr, 0};
+                    plan.splits, plan.lg, static_cast<float*>(ws), nullptr};
     tr.pl = tr.po + tr.splits * rows * a.head_dim;
     const int hd = a.head_dim;
     const bool duo = attn_duo_enabled() && plan.ctas > kGb300Sms;      // as for launch_attention_tc
     cudaError_t e;
 #define DLO_AF(NB, TAIL, DUO)                                                                                    \
-    e = run_tc<NB, TAIL, DUO, kTrain>(Q, K, V, O, a.batch, a.heads, hd, a.nq, a.nk, a.ldq, a.ldk, a.ldv, a.ldo, err, \
+    e = run_tc<NB, TAIL, DUO, true>(Q, K, V, O, a.batch, a.heads, hd, a.nq, a.nk, a.ldq, a.ldk, a.ldv, a.ldo, err, \
                                     s, launches, tr)
     if (hd <= 64) {
         if (duo) DLO_AF(1, false, true);
@@ -735,69 +696,7 @@ cudaError_t launch_attention_fwd(const dlo_attn& a, const void* Q, const void* K
 #undef DLO_AF
     if (e != cudaSuccess || tr.splits == 1) return e;
     e = launch_k(attn_join_kernel, static_cast<unsigned>((rows + 7) / 8), 256, 0, s, tr.po, tr.pl, tr.splits, rows, a.nq,
-                 a.heads, hd, static_cast<__nv_bfloat16*>(O), a.ldo, lse, nullptr, 0);
-    ++*launches;
-    return e != cudaSuccess ? e : cudaGetLastError();
-}
-
-namespace {
-
-// The grid of a packed forward, from the sizes alone (the lengths are on the
-// device).
-//  gh: the divisor of the group that makes the fewest tiles.  A sequence costs a part
-//    of a tile a head, or a part of a tile for all heads that share it.
-//  splits: as for the padded form, over the mean length of the keys.
-struct PackedPlan {
-    int gh, splits;
-    long long ctas;
-};
-
-PackedPlan attn_packed_plan(const dlo_attn_packed& a) {
-    const int group = a.heads / a.kv_heads;
-    const auto tiles = [&](int gh) { return static_cast<long long>(packed_slots(a.rows_q, a.batch, TQ / gh)) * (a.heads / gh); };
-    PackedPlan p = {1, 1, 0};
-    for (int gh = 2; gh <= TQ && gh <= group; ++gh)
-        if (group % gh == 0 && tiles(gh) < tiles(p.gh)) p.gh = gh;
-    const long long ctas = tiles(p.gh), fill = kGb300Sms / ctas, keys = (a.rows_k / a.batch + TK - 1) / TK / 4;
-    const long long n = fill < keys ? fill : keys;
-    p.splits = static_cast<int>(n < 1 ? 1 : n > 64 ? 64 : n);
-    p.ctas = ctas * p.splits;
-    return p;
-}
-
-}  // namespace
-
-size_t attention_packed_fwd_workspace(const dlo_attn_packed& a) {
-    const int n = attn_packed_plan(a).splits;
-    return 256 + (n > 1 ? static_cast<size_t>(n) * a.heads * a.rows_q * (a.head_dim + 1) * sizeof(float) : 0);
-}
-
-cudaError_t launch_attention_packed_fwd(const dlo_attn_packed& a, const void* Q, const void* K, const void* V, void* O,
-                                        float* lse, void* ws, int* err, cudaStream_t s, unsigned long long* launches) {
-    const size_t rows = static_cast<size_t>(a.heads) * a.rows_q;
-    const PackedPlan plan = attn_packed_plan(a);
-    AttnTrain tr = {lse, a.q_starts, a.k_starts, a.causal_block < a.rows_k ? a.causal_block : a.rows_k, a.heads / a.kv_heads,
-                    plan.splits, plan.gh, static_cast<float*>(ws), nullptr, a.batch};
-    tr.pl = tr.po + tr.splits * rows * a.head_dim;
-    const int hd = a.head_dim;
-    const bool duo = attn_duo_enabled() && plan.ctas > kGb300Sms;      // as for launch_attention_tc
-    cudaError_t e;
-#define DLO_AP(NB, TAIL, DUO)                                                                                       \
-    e = run_tc<NB, TAIL, DUO, kPacked>(Q, K, V, O, 1, a.heads, hd, a.rows_q, a.rows_k, a.ldq, a.ldk, a.ldv, a.ldo, err, \
-                                       s, launches, tr)
-    if (hd <= 64) {
-        if (duo) DLO_AP(1, false, true);
-        else DLO_AP(1, false, false);
-    } else if (hd <= 80) {
-        if (duo) DLO_AP(1, true, true);
-        else DLO_AP(1, true, false);
-    } else {
-        DLO_AP(2, false, false);
-    }
-#undef DLO_AP
-    if (e != cudaSuccess || tr.splits == 1) return e;
-    e = launch_k(attn_join_kernel, static_cast<unsigned>((rows + 7) / 8), 256, 0, s, tr.po, tr.pl, tr.splits, rows,
-                 a.rows_q, a.heads, hd, static_cast<__nv_bfloat16*>(O), a.ldo, lse, a.q_starts, a.batch);
+                 a.heads, hd, static_cast<__nv_bfloat16*>(O), a.ldo, lse);
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -125,6 +125,31 @@ __device__ __forceinline__ bool grid_arrive_wait(unsigned* count, unsigned n, co
     }
 }
 
+// ------------------------------------------------------------------ work of CTAs not yet launched
+// A running CTA takes over the index of one of its grid's CTAs that has not been launched:
+// the request's 16-byte answer lands in shared memory as transaction bytes on `bar`.
+// After an answer that there is none left, no further request may be made, and a CTA
+// that asked waits for the answer before it ends.
+
+__device__ __forceinline__ void cta_request(uint32_t answer, uint32_t bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+                 "r"(bar)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool cta_answer(uint32_t answer, int& x, int& y) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 a;\n\t.reg .b32 z, w;\n\tld.shared.b128 a, [%3];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, a;\n\tselp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, z, w}, a;\n\t}"
+        : "=&r"(ok), "=&r"(x), "=&r"(y)
+        : "r"(answer)
+        : "memory");
+    return ok != 0;
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const void* tmap) {

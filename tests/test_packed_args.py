@@ -147,16 +147,20 @@ def packed_tile(starts, batch, rows, t, slot):
     """The kernels' search for the tile of a slot, a lane at a time (attention.cuh: packed_tile)."""
     at = lambda b: min(max(starts[b], 0), rows)          # noqa: E731
     b, n = 0, batch
-    while n > 1:
-        step = (n + 31) // 32
-        before = [lane for lane in range(32) if lane * step < n and at(b + lane * step) // t + b + lane * step <= slot]
+    while True:
+        step = (n + 30) // 31
+        index = [b + min(lane * step, n) for lane in range(32)]
+        assert all(0 <= i <= batch for i in index)
+        before = [lane for lane in range(32) if lane * step < n and at(index[lane]) // t + index[lane] <= slot]
         k = before[-1] if before else 0
+        if step == 1:
+            row0, end = at(index[k]), at(index[k + 1])
+            b += k
+            break
         b += k * step
         n = min(step, n - k * step)
-    row0 = at(b)
-    length = max(0, at(b + 1) - row0)
     tile = slot - (row0 // t + b)
-    return (b, tile if tile * t < length else -1)
+    return (b, tile if tile * t < max(0, end - row0) else -1)
 
 
 @pytest.mark.parametrize("t", [128, 25, 1])
