@@ -44,6 +44,35 @@ __device__ __forceinline__ void put_row(uint8_t* tile, int row, int c, const uin
     }
 }
 
+// 32 columns of 32 rows, one row a lane (w: 16 pairs of bf16), to global memory: row(r)
+// is where row (lane & ~3) + r of the warp begins (its column 0; NULL: not written), c32
+// the first column, hd the columns of a row.  Four lanes first exchange their rows' 16-byte
+// pieces, so that an instruction writes 64 bytes of eight rows; 16 bytes of 32 rows take
+// four times the cycles (the end of a dK, dV item at head dim 128: 4.4 us).
+template <typename Row>
+__device__ __forceinline__ void put_rows32(uint32_t (&w)[16], int c32, int hd, int lane, const Row& row) {
+#pragma unroll
+    for (int x = 1; x <= 2; x <<= 1) {
+        const bool up = lane & x;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & x) continue;             // pieces k and k + x change places across lanes that differ by x
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                uint32_t &a = w[4 * k + u], &b = w[4 * (k + x) + u];
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, x);
+                if (up) a = got;
+                else b = got;
+            }
+        }
+    }
+    const int col = c32 + 8 * (lane & 3);
+    if (col >= hd) return;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        if (__nv_bfloat16* p = row(r)) *reinterpret_cast<uint4*>(p + col) = make_uint4(w[4 * r], w[4 * r + 1], w[4 * r + 2], w[4 * r + 3]);
+}
+
 template <int NB, bool TAIL>
 __device__ __forceinline__ void store_tile(uint32_t src, const CUtensorMap* main, const CUtensorMap* tail, int h, int row0, int b) {
     using T = AttnTile<NB, TAIL>;

@@ -161,33 +161,34 @@ __device__ __forceinline__ void put_rows(const PackedArgs& g, const Item& it, ui
         (whole ? g.lse : g.pl)[whole ? at : part] = lse;
         if (g.parts > 1 && it.part == 0) g.count[at] = it.parts;
     }
-    __nv_bfloat16* orow = g.O + (static_cast<size_t>(it.q0) + i) * g.ldo + head * g.hd;
-    // a part without a key is not read by the join
-    const bool put = live && (whole || !none);
+    // where rows (lane & ~3) + 0..3 of the warp begin
+    __nv_bfloat16* to[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = (row & ~3) + k, q = it.qi + r / g.gh;
+        to[k] = r < TQ / g.gh * g.gh && q < it.nq ? g.O + (static_cast<size_t>(it.q0) + q) * g.ldo + (it.head + r % g.gh) * g.hd : nullptr;
+    }
 #pragma unroll 1
     for (int k = 0; k < (HDP + 31) / 32; ++k) {
         uint32_t r[32];
         tmem_ld_32x32b_x32(o + k * 32, r);
         tmem_wait_ld_r(r);
-        if (!put) continue;
         if (none) {
 #pragma unroll
             for (int u = 0; u < 32; ++u) r[u] = 0;
         }
+        if (whole) {
+            uint32_t w[16];
 #pragma unroll
-        for (int u = 0; u < 32; u += 8) {
-            if (k * 32 + u >= g.hd) break;
-            float f[8];
+            for (int u = 0; u < 16; ++u) w[u] = pack_bf16x2(__uint_as_float(r[2 * u]) * inv, __uint_as_float(r[2 * u + 1]) * inv);
+            put_rows32(w, k * 32, g.hd, row & 31, [&](int i) { return to[i]; });
+        } else if (live && !none) {      // the join does not read a part without a key
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(r[u + e]) * inv;
-            if (!whole) {
-                float4* p = reinterpret_cast<float4*>(g.po + part * g.hd + k * 32 + u);
-                p[0] = make_float4(f[0], f[1], f[2], f[3]);
-                p[1] = make_float4(f[4], f[5], f[6], f[7]);
-            } else {
-                *reinterpret_cast<uint4*>(orow + k * 32 + u) =
-                    make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-            }
+            for (int u = 0; u < 32; u += 4)
+                if (k * 32 + u < g.hd)
+                    *reinterpret_cast<float4*>(g.po + part * g.hd + k * 32 + u) =
+                        make_float4(__uint_as_float(r[u]) * inv, __uint_as_float(r[u + 1]) * inv, __uint_as_float(r[u + 2]) * inv,
+                                    __uint_as_float(r[u + 3]) * inv);
         }
     }
 }

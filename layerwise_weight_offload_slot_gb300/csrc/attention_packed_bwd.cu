@@ -176,27 +176,34 @@ __device__ __forceinline__ bool take_item(const PackedBwdBars& m, const BwdItem*
     return true;
 }
 
-// Columns [32 c, 32 c + 32) of one accumulator row times `scale` to its row of the gradient, or
-// (part) in fp32 to its part.  `live`: the row is the sequence's; `none`: zeros, for a
-// row without a visible pair.  The whole warp reads.
-__device__ __forceinline__ void put_chunk(uint32_t t, int c, __nv_bfloat16* out, float* part, int hd, bool live, bool none, float scale) {
+// Columns [32 c, 32 c + 32) of the warp's accumulator rows times `scale` to their rows of the
+// gradient (out: that of the warp's row 0; rows: how many of its 32 are the sequence's), or
+// (part, this lane's row) in fp32 to their part.  `none`: zeros, for a row without a
+// visible pair.  The whole warp reads.
+__device__ __forceinline__ void put_chunk(uint32_t t, int c, __nv_bfloat16* out, int ld, int rows, float* part, int hd, int lane,
+                                          bool none, float scale) {
     uint32_t r[32];
     tmem_ld_32x32b_x32(t + c * 32, r);
     tmem_wait_ld_r(r);
-    if (!live) return;
+    if (none) {
 #pragma unroll
-    for (int u = 0; u < 32; u += 8) {
-        if (c * 32 + u >= hd) break;
-        float f[8];
+        for (int u = 0; u < 32; ++u) r[u] = 0;
+    }
+    if (part) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = none ? 0.f : __uint_as_float(r[u + e]) * scale;
-        if (part) {
-            reinterpret_cast<float4*>(part + c * 32 + u)[0] = make_float4(f[0], f[1], f[2], f[3]);
-            reinterpret_cast<float4*>(part + c * 32 + u)[1] = make_float4(f[4], f[5], f[6], f[7]);
-        } else {
-            *reinterpret_cast<uint4*>(out + c * 32 + u) =
-                make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-        }
+        for (int u = 0; u < 32; u += 4)
+            if (lane < rows && c * 32 + u < hd)
+                *reinterpret_cast<float4*>(part + c * 32 + u) =
+                    make_float4(__uint_as_float(r[u]) * scale, __uint_as_float(r[u + 1]) * scale, __uint_as_float(r[u + 2]) * scale,
+                                __uint_as_float(r[u + 3]) * scale);
+    } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) w[u] = pack_bf16x2(__uint_as_float(r[2 * u]) * scale, __uint_as_float(r[2 * u + 1]) * scale);
+        put_rows32(w, c * 32, hd, lane, [&](int k) -> __nv_bfloat16* {
+            const int i = (lane & ~3) + k;
+            return i < rows ? out + static_cast<size_t>(i) * ld : nullptr;
+        });
     }
 }
 
@@ -446,6 +453,12 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         float* parts = reinterpret_cast<float*>(smem + P::SEL_OFF) + row;
         bool ok = true;
         int t = 0, ns = 0, nd = 0, nt = 0, na = 0;      // steps; S, dP, one-tile items, items so far
+        const auto row_lse = [&](const BwdItem& it) {
+            const int i = it.tile * kTile + row;
+            return i < it.nq ? g.lse[static_cast<size_t>(it.head) * g.rows_q + it.q0 + i] : -INFINITY;
+        };
+        float l = 0.f;                // of the coming item's row, where `early`
+        bool early = false;
         for (int item = 0;; ++item) {
             const BwdItem& it = items[item % kItems];
             ok = warp_wait(m.item_full + 8 * (item % kItems), (item / kItems) & 1, abort_flag);
@@ -458,11 +471,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             int end = 1 << 30;
             {
                 const int i = it.tile * kTile + row;
-                if (i < it.nq) {
-                    end = key_end(i, it.nk - it.nq, g.causal_block, it.nk) - it.i0 * kTile;
-                    const float l = g.lse[static_cast<size_t>(it.head) * g.rows_q + it.q0 + i];
-                    if (l != -INFINITY) l2 = l * 1.4426950408889634f;
-                }
+                if (i < it.nq) end = key_end(i, it.nk - it.nq, g.causal_block, it.nk) - it.i0 * kTile;
+                if (!early) l = row_lse(it);
+                if (l != -INFINITY) l2 = l * 1.4426950408889634f;
             }
             const uint64_t neg_l2 = f32x2(-l2, -l2);
             uint64_t neg_d = 0;
@@ -560,18 +571,25 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
             if (!ok) break;
             t += n;
+            // the next item's row statistic is on its way while this one's gradient is written
+            // (its load would hold up that item's first step by a microsecond)
+            const BwdItem& next = items[(item + 1) % kItems];
+            early = __all_sync(0xFFFFFFFFu, mbar_try_wait(m.item_full + 8 * ((item + 1) % kItems), ((item + 1) / kItems) & 1));
+            if (early && next.n >= 0) l = row_lse(next);
             if (n > 0) {
                 ok = warp_wait(m.done, na & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
                 ++na;
             }
-            const int i = it.tile * kTile + row;
-            const size_t at = static_cast<size_t>(it.q0) + i;
-            float* part = g.splits_q == 1 ? nullptr
-                                          : g.part_q + ((static_cast<size_t>(it.split) * g.rows_q + at) * g.heads + it.head) * g.hd;
+            const int i0 = it.tile * kTile + (warp & 3) * 32;         // the warp's first row
+            const size_t at = static_cast<size_t>(it.q0) + i0;
+            float* part = g.splits_q == 1
+                              ? nullptr
+                              : g.part_q + ((static_cast<size_t>(it.split) * g.rows_q + at + lane) * g.heads + it.head) * g.hd;
             for (int c = e; c < (T::HDP + 31) / 32; c += kGroups)
-                put_chunk(tl + 384, c, g.dQ + at * g.lddq + it.head * g.hd, part, g.hd, i < it.nq, n == 0 || end <= 0, g.scale);
+                put_chunk(tl + 384, c, g.dQ + at * g.lddq + it.head * g.hd, g.lddq, it.nq - i0, part, g.hd, lane, n == 0 || end <= 0,
+                          g.scale);
             // dQ's columns are read before the e0 that lets the next item's first product write them
             tc_fence_before();
             __syncwarp();
@@ -986,14 +1004,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             }
             // even groups bring dV, odd ones dK
             const bool k = e & 1;
-            const size_t at = static_cast<size_t>(it.k0) + it.tile * kTile + row;
-            const bool live = it.tile * kTile + row < it.nk;
+            const int i0 = it.tile * kTile + (warp & 3) * 32;         // the warp's first row
+            const size_t at = static_cast<size_t>(it.k0) + i0;
             float* part = g.splits_k == 1 ? nullptr
                                           : (k ? g.part_k : g.part_v) +
-                                                ((static_cast<size_t>(it.split) * g.rows_k + at) * g.kv_heads + it.head) * g.hd;
+                                                ((static_cast<size_t>(it.split) * g.rows_k + at + lane) * g.kv_heads + it.head) * g.hd;
             __nv_bfloat16* out = (k ? g.dK + at * g.lddk : g.dV + at * g.lddv) + it.head * g.hd;
             for (int c = e >> 1; c < (T::HDP + 31) / 32; c += kGroups / 2)
-                put_chunk(tl + (k ? M::DK_COL : M::DV_COL), c, out, part, g.hd, live, n == 0 || begin >= it.nq, k ? g.scale : 1.f);
+                put_chunk(tl + (k ? M::DK_COL : M::DV_COL), c, out, k ? g.lddk : g.lddv, it.nk - i0, part, g.hd, lane,
+                          n == 0 || begin >= it.nq, k ? g.scale : 1.f);
             // read before the e0 and e1 that let the next item's first products write there
             tc_fence_before();
             __syncwarp();
