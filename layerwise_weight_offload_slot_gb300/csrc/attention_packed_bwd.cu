@@ -545,6 +545,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                     if (lane == 0) mbar_arrive(m.e1);
                     if (!warp_wait(m.e1, par >> 2 & 1, abort_flag)) { ok = false; break; }
                     par ^= 4;
+                    tc_fence_after();
                     d = (parts[0] + parts[kTile]) + (parts[2 * kTile] + parts[3 * kTile]);
                     neg_d = f32x2(-d, -d);
                     write_stats(d);

@@ -94,10 +94,19 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* grids, co
 //
 // Bound by memory: x is read and y written once, 16 bytes a thread where the pairs
 // allow it.  A row's sines and cosines are formed once, in shared memory, while the
-// first loads of x are in flight; then a thread keeps the columns of its place in
-// the head for every head that it walks, so its sines and cosines stay in registers.
+// first loads of x are in flight.  A thread keeps its columns of the head and walks
+// heads of one row (wide rows: its sines and cosines stay in registers) or rows (ROWS:
+// narrow ones, where a row gives it less than three heads), a few ahead.
 constexpr int kRopeThreads = 256;
-constexpr int kRopeAhead = 4;                // heads of a thread with loads in flight
+
+// Pieces of a thread with loads in flight, and CTAs an SM: a piece of the half layout
+// is two loads, its registers are two and a half times the others' (8192 rows of 80
+// heads of 128: 51.6 us, 55 with four pieces and three CTAs, 58.8 with two and five;
+// interleaved 50.5, 53.6 where the compiler takes what it likes).
+template <int V, bool HALF>
+constexpr int kAhead = V == 8 && HALF ? 3 : 4;
+template <int V, bool HALF>
+constexpr int kCtas = V == 8 && HALF ? 4 : 6;
 
 struct RopeArgs {
     const __nv_bfloat16* x;
@@ -107,7 +116,7 @@ struct RopeArgs {
     int rows, heads, hd, pairs, axes, ldx, ldy;
     int end[DLO_ROPE_AXES];                  // one past the last pair of each axis
     int turned, items;                       // pieces of a head: turned ones first, then copied ones
-    int ny, nr;                              // heads side by side and rows of a CTA
+    int ny, nr;                              // heads and rows side by side in a CTA
     float amp, amp_sin;                      // amp_sin = -amp in the backward pass
 };
 
@@ -118,20 +127,33 @@ struct RopeVec {                             // V bf16 columns
         if constexpr (V == 8) {
             const uint4 u = *reinterpret_cast<const uint4*>(p);
             w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-        } else if constexpr (V == 4) {
-            const uint2 u = *reinterpret_cast<const uint2*>(p);
-            w[0] = u.x, w[1] = u.y;
         } else if constexpr (V == 2) {
             w[0] = *reinterpret_cast<const uint32_t*>(p);
-        } else {
+        } else if constexpr (V == 1) {
             w[0] = *reinterpret_cast<const uint16_t*>(p);
+        } else {
+            load_half(p, true);
         }
     }
     __device__ void store(__nv_bfloat16* p) const {
         if constexpr (V == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-        else if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
         else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
-        else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+        else if constexpr (V == 1) *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(w[0]);
+        else store_half(p, true);
+    }
+    // by 8 bytes; of eight columns the second four only where `whole`
+    __device__ void load_half(const __nv_bfloat16* p, bool whole) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        w[0] = u.x, w[1] = u.y;
+        if constexpr (V == 8) {
+            const uint2 v = whole ? *reinterpret_cast<const uint2*>(p + 4) : make_uint2(0, 0);
+            w[2] = v.x, w[3] = v.y;
+        }
+    }
+    __device__ void store_half(__nv_bfloat16* p, bool whole) const {
+        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        if constexpr (V == 8)
+            if (whole) *reinterpret_cast<uint2*>(p + 4) = make_uint2(w[2], w[3]);
     }
     __device__ float get(int i) const {
         return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
@@ -142,91 +164,118 @@ struct RopeVec {                             // V bf16 columns
 };
 
 // HALF: a piece is V columns of the first half of the turned part and their partners
-// in the second; else V columns, V / 2 pairs side by side.
-template <int V, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs g) {
-    extern __shared__ float2 turn[];         // [nr][pairs]: amp cos, amp sin
+// in the second; else V columns, V / 2 pairs side by side.  ODD (HALF, V = 8, pairs = 4
+// mod 8, as a head of 72 has): the partners lie on 8-byte boundaries and the last
+// piece has four columns (16381 rows of 48 heads of 96, 72 columns turned: 58.5 us, 60.5
+// in pieces of four columns).
+template <int V, bool HALF, bool ROWS, bool ODD>
+__global__ void __launch_bounds__(kRopeThreads, kCtas<V, HALF>) rope_kernel(const __grid_constant__ RopeArgs g) {
+    extern __shared__ float2 turn[];         // [rows of the CTA][pairs]: amp cos, amp sin
     constexpr int P = HALF ? V : V / 2;      // pairs of a piece
+    constexpr int A = kAhead<V, HALF>;
+    constexpr int R = ROWS ? A : 1; // rows of a thread
     const int c = threadIdx.x % g.items, q = threadIdx.x / g.items, h0 = q % g.ny, rr = q / g.ny;
-    const long long first = static_cast<long long>(blockIdx.x) * g.nr, row = first + rr;
-    const bool in = rr < g.nr && row < g.rows, turned = c < g.turned;
+    const long long first = static_cast<long long>(blockIdx.x) * g.nr * R;
+    const int rows = static_cast<int>(min(static_cast<long long>(g.nr) * R, g.rows - first));
+    const int heads = rr < g.nr && rr < rows ? g.heads : 0;
+    const bool turned = c < g.turned, whole = !ODD || !turned || (c + 1) * V <= g.pairs;
     const int half = HALF ? g.pairs : 0;     // columns between partners
     const int col = turned ? c * V : 2 * g.pairs + (c - g.turned) * V;
-    const __nv_bfloat16* x = g.x + row * g.ldx + col;
-    __nv_bfloat16* y = g.y + row * g.ldy + col;
-    RopeVec<V> a[kRopeAhead], b[HALF ? kRopeAhead : 1];
+    const __nv_bfloat16* x = g.x + (first + rr) * g.ldx + col;
+    __nv_bfloat16* y = g.y + (first + rr) * g.ldy + col;
+    // piece k of a batch: head h + k ny of the row, or row rr + k nr of the head
+    const long long step_x = ROWS ? static_cast<long long>(g.nr) * g.ldx : static_cast<long long>(g.ny) * g.hd;
+    const long long step_y = ROWS ? static_cast<long long>(g.nr) * g.ldy : step_x;
+    const auto there = [&](int h, int k) { return ROWS ? rr + k * g.nr < rows : h + k * g.ny < heads; };
+    RopeVec<V> a[A], b[HALF ? A : 1];
     pdl_wait();
     pdl_launch_dependents();
     const auto load = [&](int h) {
+        const __nv_bfloat16* p = x + h * g.hd;
 #pragma unroll
-        for (int k = 0; k < kRopeAhead; ++k) {
-            const int at = h + k * g.ny;
-            if (in && at < g.heads) {
-                a[k].load(x + at * g.hd);
-                if (HALF && turned) b[k].load(x + at * g.hd + half);
+        for (int k = 0; k < A; ++k, p += step_x) {
+            if (!there(h, k)) break;
+            if (ODD && !whole) a[k].load_half(p, false);
+            else a[k].load(p);
+            if constexpr (HALF) {
+                if (turned) {
+                    if constexpr (ODD) b[k].load_half(p + half, whole);
+                    else b[k].load(p + half);
+                }
             }
         }
     };
-    load(h0);
-    const int rows = static_cast<int>(min(static_cast<long long>(g.nr), g.rows - first));
+    if (h0 < heads) load(h0);
     for (int i = threadIdx.x; i < rows * g.pairs; i += kRopeThreads) {
         const int r = i / g.pairs, p = i - r * g.pairs;
         int axis = 0;
         while (p >= g.end[axis]) ++axis;     // end[axes - 1] = pairs
-        const long long n = g.positions[(first + r) * g.axes + axis];
-        const uint64_t phase = static_cast<uint64_t>(n) * g.steps[p];
+        const long long at = g.positions[(first + r) * g.axes + axis];
+        const uint64_t phase = static_cast<uint64_t>(at) * g.steps[p];
         float s, co;
         sincospif(static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f, &s, &co);   // 2^-31
         turn[i] = make_float2(g.amp * co, g.amp_sin * s);
     }
     __syncthreads();
     float2 t[P > 0 ? P : 1];
-    if (in && turned) {
+    const auto turns = [&](int r) {
 #pragma unroll
-        for (int p = 0; p < P; ++p) t[p] = turn[rr * g.pairs + c * P + p];
-    }
-    for (int h = h0; h < g.heads; h += kRopeAhead * g.ny) {
+        for (int p = 0; p < P; ++p) t[p] = whole || p < P / 2 ? turn[r * g.pairs + c * P + p] : make_float2(0.f, 0.f);
+    };
+    if (!ROWS && turned && heads) turns(rr);
+    for (int h = h0; h < heads; h += ROWS ? g.ny : A * g.ny) {
         if (h != h0) load(h);
+        __nv_bfloat16* to = y + h * g.hd;
 #pragma unroll
-        for (int k = 0; k < kRopeAhead; ++k) {
-            const int at = h + k * g.ny;
-            if (!in || at >= g.heads) continue;
-            if (turned) {
-                if constexpr (HALF) {
-                    RopeVec<V> u, w;
+        for (int k = 0; k < A; ++k, to += step_y) {
+            if (!there(h, k)) break;
+            if (!turned) {
+                a[k].store(to);
+                continue;
+            }
+            if (ROWS) turns(rr + k * g.nr);
+            if constexpr (HALF) {
+                RopeVec<V> u, w;
 #pragma unroll
-                    for (int p = 0; p < V; p += 2) {
-                        const int p1 = V > 1 ? p + 1 : p;
-                        const float u0 = a[k].get(p), u1 = a[k].get(p1), v0 = b[k].get(p), v1 = b[k].get(p1);
-                        u.put(p, u0 * t[p].x - v0 * t[p].y, u1 * t[p1].x - v1 * t[p1].y);
-                        w.put(p, u0 * t[p].y + v0 * t[p].x, u1 * t[p1].y + v1 * t[p1].x);
-                    }
-                    u.store(y + at * g.hd);
-                    w.store(y + at * g.hd + half);
-                } else {
-#pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        const float u = a[k].get(2 * p), v = a[k].get(2 * p + 1);
-                        a[k].put(2 * p, u * t[p].x - v * t[p].y, u * t[p].y + v * t[p].x);
-                    }
-                    a[k].store(y + at * g.hd);
+                for (int p = 0; p < V; p += 2) {
+                    const int p1 = V > 1 ? p + 1 : p;
+                    const float u0 = a[k].get(p), u1 = a[k].get(p1), v0 = b[k].get(p), v1 = b[k].get(p1);
+                    u.put(p, u0 * t[p].x - v0 * t[p].y, u1 * t[p1].x - v1 * t[p1].y);
+                    w.put(p, u0 * t[p].y + v0 * t[p].x, u1 * t[p1].y + v1 * t[p1].x);
                 }
+                if (ODD && !whole) u.store_half(to, false);
+                else u.store(to);
+                if constexpr (ODD) w.store_half(to + half, whole);
+                else w.store(to + half);
             } else {
-                a[k].store(y + at * g.hd);
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+                    const float u = a[k].get(2 * p), v = a[k].get(2 * p + 1);
+                    a[k].put(2 * p, u * t[p].x - v * t[p].y, u * t[p].y + v * t[p].x);
+                }
+                a[k].store(to);
             }
         }
     }
 }
 
-template <int V, bool HALF>
+template <int V, bool HALF, bool ODD = false>
 cudaError_t run_rope(RopeArgs g, cudaStream_t s) {
     const int copied = g.x == g.y ? 0 : (g.hd - 2 * g.pairs) / V;
-    g.turned = HALF ? g.pairs / V : 2 * g.pairs / V;
+    g.turned = HALF ? (g.pairs + V - 1) / V : 2 * g.pairs / V;
     g.items = g.turned + copied;
-    g.ny = kRopeThreads / g.items < g.heads ? kRopeThreads / g.items : g.heads;
+    // as many heads side by side as fit, evenly over the passes that the row takes
+    const int fit = kRopeThreads / g.items, passes = (g.heads + fit - 1) / fit;
+    g.ny = (g.heads + passes - 1) / passes;
     g.nr = kRopeThreads / (g.items * g.ny);
-    return launch_k(rope_kernel<V, HALF>, static_cast<unsigned>((g.rows + g.nr - 1) / g.nr), kRopeThreads,
-                    static_cast<size_t>(g.nr) * g.pairs * sizeof(float2), s, g);
+    constexpr int A = kAhead<V, HALF>;
+    // rows ahead, unless that leaves SMs without a CTA
+    const bool ahead = passes < 3 && static_cast<long long>(g.rows) >= static_cast<long long>(kGb300Sms) * g.nr * A;
+    const int rows = g.nr * (ahead ? A : 1);
+    const unsigned ctas = static_cast<unsigned>((static_cast<long long>(g.rows) + rows - 1) / rows);
+    const size_t smem = static_cast<size_t>(rows) * g.pairs * sizeof(float2);
+    return ahead ? launch_big<rope_kernel<V, HALF, true, ODD>>(ctas, kRopeThreads, smem, s, g)
+                 : launch_big<rope_kernel<V, HALF, false, ODD>>(ctas, kRopeThreads, smem, s, g);
 }
 
 }  // namespace
@@ -255,12 +304,12 @@ cudaError_t launch_rope(const dlo_rope& r, bool back, const void* x, int ldx, co
     for (int a = 0; a < r.axes; ++a) g.end[a] = g.pairs += r.axis[a].dim / 2;
     g.amp = r.amp;
     g.amp_sin = back ? -r.amp : r.amp;
-    // the widest piece that whole pairs fill: 16 bytes where the pairs are a multiple of 4
-    // (interleaved) or 8 (half layout: heads of 64 and 128; 8 bytes for 72), down to a column
+    // the widest piece that whole pairs fill: 16 bytes where the pairs are a multiple of 4,
+    // down to a column of 2
     cudaError_t e;
     if (r.layout == DLO_ROPE_HALF) {
         e = g.pairs % 8 == 0   ? run_rope<8, true>(g, s)
-            : g.pairs % 4 == 0 ? run_rope<4, true>(g, s)
+            : g.pairs % 8 == 4 ? run_rope<8, true, true>(g, s)
             : g.pairs % 2 == 0 ? run_rope<2, true>(g, s)
                                : run_rope<1, true>(g, s);
     } else {
