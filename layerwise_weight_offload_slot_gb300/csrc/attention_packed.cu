@@ -25,7 +25,19 @@
 // Barriers and buffers run on through the items: tile j of an item that began with c
 // tiles behind it is tile c + j.
 //
-// DUO (head dims up to 80): two CTAs on an SM, one S buffer each, as there.
+// DUO (head dims up to 80): two CTAs on an SM, one S buffer each, as there (24 images of
+// 16 x 72: 51.5 us, 54.4 with one CTA an SM).
+//
+// What bounds it.  Long sequences: the products and the softmax, 0.85 us a tile at head
+// dim 128, as in attention_tc.cu (8192 tokens, 40 heads: 896 us, 1534 TFLOP/s).  Short ones:
+// an item of 4 tiles takes 5.9 us, 2.5 of them its end, where the softmax warps wait for the
+// last product (0.3), write O (1.6) and begin the next (16 x 512 tokens, 40 heads of 128:
+// 100 us, tensor pipe 34% active; a CTA an item took 150).  Single queries: memory (64 x
+// 4096 keys, 8 key/value heads of 128: 168 us, 6.4 TB/s, 0.94 of the measured copy); with
+// unequal lengths the last items (24 sequences of 422 to 7173 keys: 73 us, 5.5 TB/s).
+// Measured and not kept: O in two buffers and four warps more that write it (12 warps leave
+// 168 registers a thread: 109 us where 100; with setmaxnreg the compiler spills 1232 bytes),
+// two chunks of O at once (104).
 //
 // Every wait is bounded; one that runs out sets the error word and every role leaves
 // its loops, with loads, requests and MMAs in flight waited for.
@@ -307,7 +319,8 @@ __global__ void __launch_bounds__(kThreadsP, DUO ? 2 : 1)
                 c += it.n;
             }
             // the next one, asked for only now: a CTA that asks early keeps the item from others
-            // that are done sooner (9 prompts, 40 heads over 8: 553 us instead of 4xx).  The
+            // that are done sooner (24 single queries over 98304 keys: 94 us, 128 when it asked at the
+            // item's start; steps ahead of the last load measured the same as behind it).  The
             // answer has to land before this CTA may end
             if (!ok) break;
             if (lane == 0) {
@@ -514,7 +527,7 @@ __global__ void __launch_bounds__(kThreadsP, DUO ? 2 : 1)
                     uint32_t w[16];
                     // no row of the warp sees these keys: p = 0, as the exponentials would
                     // give.  Worth its branch where two CTAs share the SM (24 images of 16 x
-                    // 72: 57 us against 60), not where one has it (3% slower)
+                    // 72: 57 us against 60 at the time), not where one has it (3% slower)
                     if (DUO && k * 32 >= warp_end - j * TK) {
 #pragma unroll
                         for (int u = 0; u < 16; ++u) w[u] = 0;

@@ -16,6 +16,14 @@
 // completes `raw` of its slot, and warp 3 then completes `full`.  Elsewhere they stay
 // in their own rows, which are not written.
 //
+// What bounds it: for long sequences the tensor core and, in dQ, the elementwise warps'
+// chain of waits, loads and stores (1.13 us a step at head dim 128; attention_bwd.cu's
+// kernels, whose loops know where their slots begin, are 5% faster there: 8192 tokens, 40
+// heads, 2600 us, these 2720); for short ones the change of items, ~3 us each: the last
+// product, the gradient's way out (~0.9), K and V (Q, dO and O) from L2 (1.2) and the first
+// products.  16 x 512 tokens of 40 heads of 128: 261 us (dQ 132, tensor pipe 46% active; dK, dV
+// 140, 55%), 393 with a CTA an item.
+//
 // D = rowsum(dO O) is the diagonal of one more product, dO O^T, an item's step before
 // the first: O comes by TMA into a slot of the ring, and no thread loads and adds up
 // rows.  Rows that lie in one key tile form it from P dP instead, as there.
@@ -211,8 +219,7 @@ __device__ __forceinline__ void put_chunk(uint32_t t, int c, __nv_bfloat16* out,
 // TMEM: S [0, 128), dP [128, 256), two dS [256, 320) and [320, 384), dQ [384, 512); dO O^T
 // of an item takes dP's place before its first dP.  Order of issue as dq_kernel's, but S_j
 // goes after dQ_{j-2}: whoever has S_j may then write its dS, where a wait for the dQ before
-// cost the elementwise warps, whose chain of waits, loads and stores a step is what bounds
-// this kernel, ~0.1 us of 1.13 a step at head dim 128.
+// cost the elementwise warps 0.13 us a step (8192 tokens of 32 heads of 64: dQ 722 us, 738).
 template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     packed_dq_kernel(const __grid_constant__ PackedBwdMaps maps, const __grid_constant__ PackedBwdArgs g) {
