@@ -731,8 +731,11 @@ typedef struct dlo_attn_packed {
     const int* k_starts;
 } dlo_attn_packed;
 
+/* Workspace bytes (0: bad description), from the sizes alone: row statistics and, where few
+ * rows share long sequences, partial results (at most 512 MB of them forward). */
 size_t dlo_attention_packed_fwd_workspace_bytes(const dlo_attn_packed* a);
 size_t dlo_attention_packed_bwd_workspace_bytes(const dlo_attn_packed* a);
+/* As dlo_op_attention_fwd and dlo_op_attention_bwd; ws 256-byte aligned. */
 dlo_status dlo_op_attention_packed_fwd(const dlo_attn_packed* a, const void* Q, const void* K, const void* V, void* O,
                                        float* lse, void* ws, size_t ws_bytes, int* err, void* stream);
 dlo_status dlo_op_attention_packed_bwd(const dlo_attn_packed* a, const void* Q, const void* K, const void* V,
