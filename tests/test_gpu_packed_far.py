@@ -14,6 +14,15 @@ def stream():
     return torch.cuda.current_stream().cuda_stream
 
 
+@pytest.fixture(autouse=True)
+def float32_by_default():
+    """Another test module of the same process may have set another default."""
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(torch.float32)
+    yield
+    torch.set_default_dtype(before)
+
+
 @pytest.mark.parametrize("hd,far", [(64, 256 * 1100), (128, 256 * 1100 + 5)])
 def test_attention_of_far_rows(hd, far):
     H, G, lens, ld = 2, 1, [200, 0, 131], 8192          # 281600 rows of 8192: 2.3e9 elements a matrix
@@ -27,7 +36,7 @@ def test_attention_of_far_rows(hd, far):
         for t, s in zip((q, k, v, do), small):
             t[first:] = s
         grads = [torch.zeros((rows, ld), dtype=torch.bfloat16, device=DEV) for _ in range(3)]
-        o, lse = torch.zeros((rows, ld), dtype=torch.bfloat16, device=DEV), torch.zeros((H, rows), device=DEV)
+        o, lse = torch.zeros((rows, ld), dtype=torch.bfloat16, device=DEV), torch.zeros((H, rows), dtype=torch.float32, device=DEV)
         starts = torch.tensor([first, first + 200, first + 200, first + n], dtype=torch.int32, device=DEV)
         a = dlo.make_attn_packed(batch=3, heads=H, kv_heads=G, head_dim=hd, rows_q=rows, rows_k=rows, causal_block=1, ldq=ld, ldk=ld,
                                  ldv=ld, ldo=ld, lddq=ld, lddk=ld, lddv=ld, lddo=ld, q_starts=starts.data_ptr(), k_starts=starts.data_ptr())
