@@ -34,7 +34,7 @@
 // last product (0.3), write O (1.6) and begin the next (16 x 512 tokens, 40 heads of 128:
 // 100 us, tensor pipe 34% active; a CTA an item took 150).  Single queries: memory (64 x
 // 4096 keys, 8 key/value heads of 128: 168 us, 6.4 TB/s, 0.94 of the measured copy); with
-// unequal lengths the last items (24 sequences of 422 to 7173 keys: 73 us, 5.5 TB/s).
+// unequal lengths the last items (24 sequences of 422 to 7173 keys: 72 us, 5.6 TB/s).
 // Measured and not kept: O in two buffers and four warps more that write it (12 warps leave
 // 168 registers a thread: 109 us where 100; with setmaxnreg the compiler spills 1232 bytes),
 // two chunks of O at once (104).
@@ -131,6 +131,10 @@ __device__ __forceinline__ void find_work(const PackedArgs& g, int x, int y, Wor
         w.tile = p.tile;
         w.end = p.tile + 1;
     } else {
+        // heads side by side: CTAs that run at once read the same rows of K and V
+        const int groups = g.heads / g.gh;
+        it.head = x % groups * g.gh;
+        x /= groups;
         // a sequence without keys has one slot too, for the zeros of its rows
         const PackedTile p = packed_tile(g.k_starts, g.batch, g.rows_k, TK * g.per, x);
         if (p.tile < 0 && (p.n > 0 || x != p.row0 / (TK * g.per) + p.b)) return;
@@ -598,38 +602,54 @@ __global__ void __launch_bounds__(kThreadsP, DUO ? 2 : 1)
 }
 
 // Joins the parts of the rows that have several: lse = log sum_p exp(lse_p), O = sum_p
-// exp(lse_p - lse) O_p.  One warp a row; rows of no sequence stay as they are.
+// exp(lse_p - lse) O_p.  Four warps a row, each a quarter of its parts (one after the
+// other they are a chain of loads: 4 x 16384 keys, 8 key/value heads, in 16 parts a row, 54.7
+// us with the launch before it, 58.3 with one warp),
+// added up in their order; rows of no sequence stay as they are.
+constexpr int kJoinWarps = 4;
+
 __global__ void __launch_bounds__(256) packed_join_kernel(const __grid_constant__ PackedArgs g) {
+    __shared__ float4 sums[8][32];
     pdl_wait();
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % kJoinWarps;
     const size_t rows = static_cast<size_t>(g.heads) * g.rows_q;
-    const size_t r = (static_cast<size_t>(blockIdx.x) * 256 + threadIdx.x) >> 5;
-    if (r >= rows) return;
+    const size_t r = static_cast<size_t>(blockIdx.x) * (8 / kJoinWarps) + warp / kJoinWarps;
     const int h = static_cast<int>(r / g.rows_q), i = static_cast<int>(r - static_cast<size_t>(h) * g.rows_q);
-    if (i < seq_start(g.q_starts, 0, g.rows_q) || i >= seq_start(g.q_starts, g.batch, g.rows_q)) return;
-    const int parts = min(g.count[r], g.parts);
-    if (parts <= 1) return;                            // written by its one item
-    // lane p holds the weights of parts p and p + 32 (kParts = 64)
-    const float l0 = lane < parts ? g.pl[lane * rows + r] : -INFINITY;
-    const float l1 = lane + 32 < parts ? g.pl[(lane + 32) * rows + r] : -INFINITY;
-    float top = fmaxf(l0, l1);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
-    const float m = top == -INFINITY ? 0.f : top;
-    const float w0 = exp2f((l0 - m) * 1.4426950408889634f), w1 = exp2f((l1 - m) * 1.4426950408889634f);
-    float total = w0 + w1;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
+    int parts = 0;                                     // 0 or 1: no row, or written by its one item
+    if (r < rows && i >= seq_start(g.q_starts, 0, g.rows_q) && i < seq_start(g.q_starts, g.batch, g.rows_q))
+        parts = min(g.count[r], g.parts);
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);      // columns 4 lane .. 4 lane + 3
+    float m = 0.f, total = 0.f;
+    if (parts > 1) {
+        // lane p holds the weights of parts p and p + 32 (kParts = 64)
+        const float l0 = lane < parts ? g.pl[lane * rows + r] : -INFINITY;
+        const float l1 = lane + 32 < parts ? g.pl[(lane + 32) * rows + r] : -INFINITY;
+        float top = fmaxf(l0, l1);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, x));
+        m = top == -INFINITY ? 0.f : top;
+        const float w0 = exp2f((l0 - m) * 1.4426950408889634f), w1 = exp2f((l1 - m) * 1.4426950408889634f);
+        total = w0 + w1;
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, x);
 #pragma unroll 4
-    for (int p = 0; p < parts; ++p) {
-        const float w = __shfl_sync(0xFFFFFFFFu, p < 32 ? w0 : w1, p & 31);
-        // weight 0: nothing visible there, its O_p was not written
-        if (4 * lane < g.hd && w != 0.f) {
-            const float4 v = reinterpret_cast<const float4*>(g.po + (p * rows + r) * g.hd)[lane];
-            acc = make_float4(acc.x + w * v.x, acc.y + w * v.y, acc.z + w * v.z, acc.w + w * v.w);
+        for (int p = sub; p < parts; p += kJoinWarps) {
+            const float w = __shfl_sync(0xFFFFFFFFu, p < 32 ? w0 : w1, p & 31);
+            // weight 0: nothing visible there, its O_p was not written
+            if (4 * lane < g.hd && w != 0.f) {
+                const float4 v = reinterpret_cast<const float4*>(g.po + (p * rows + r) * g.hd)[lane];
+                acc = make_float4(acc.x + w * v.x, acc.y + w * v.y, acc.z + w * v.z, acc.w + w * v.w);
+            }
         }
+    }
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (sub != 0 || parts <= 1) return;
+#pragma unroll
+    for (int k = 1; k < kJoinWarps; ++k) {
+        const float4 v = sums[warp + k][lane];
+        acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     if (4 * lane < g.hd)
@@ -673,7 +693,7 @@ PackedGrid packed_grid(const dlo_attn_packed& a) {
     if (per < (keys + parts - 1) / parts) per = (keys + parts - 1) / parts;
     const long long ctas = static_cast<long long>(packed_slots(a.rows_k, a.batch, TK * static_cast<int>(per))) * (a.heads / p.gh);
     parts = (keys + per - 1) / per;
-    if (parts < 2 || ctas < 2 * p.ctas) return p;
+    if (parts < 2 || ctas < 2 * p.ctas || ctas > 0x7FFFFFFF) return p;
     p.per = static_cast<int>(per);
     p.parts = static_cast<int>(parts);
     p.ctas = ctas;
@@ -686,8 +706,9 @@ cudaError_t run_packed(const PackedMaps& maps, const PackedArgs& g, cudaStream_t
     constexpr auto kernel = packed_fwd_kernel<NB, TAIL, DUO>;
     static unsigned long long attr = 0;
     if (cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), P::BYTES, &attr); e != cudaSuccess) return e;
-    const dim3 grid(g.parts > 1 ? packed_slots(g.rows_k, g.batch, TK * g.per) : packed_slots(g.rows_q, g.batch, TQ / g.gh),
-                    g.heads / g.gh);
+    const int groups = g.heads / g.gh;
+    const dim3 grid = g.parts > 1 ? dim3(packed_slots(g.rows_k, g.batch, TK * g.per) * groups)
+                                  : dim3(packed_slots(g.rows_q, g.batch, TQ / g.gh), groups);
     cudaError_t e = launch_k(kernel, grid, kThreadsP, P::BYTES, s, maps, g);
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
@@ -744,7 +765,7 @@ cudaError_t launch_attention_packed_fwd(const dlo_attn_packed& a, const void* Q,
     else if (tail) e = duo ? run_packed<1, true, true>(m, g, s, launches) : run_packed<1, true, false>(m, g, s, launches);
     else e = run_packed<2, false, false>(m, g, s, launches);
     if (e != cudaSuccess || g.parts == 1) return e;
-    e = launch_k(packed_join_kernel, static_cast<unsigned>((rows + 7) / 8), 256, 0, s, g);
+    e = launch_k(packed_join_kernel, static_cast<unsigned>((rows + 8 / kJoinWarps - 1) / (8 / kJoinWarps)), 256, 0, s, g);
     ++*launches;
     return e != cudaSuccess ? e : cudaGetLastError();
 }
