@@ -75,7 +75,7 @@ struct PackedBwdPlan {
     static constexpr int ITEM_OFF = DQ ? SEL_OFF + kGroups * kTile * 4 : STAT_OFF + STATS * kStatBytes;
     static constexpr int ANSWER_OFF = ITEM_OFF + kItems * static_cast<int>(sizeof(BwdItem));
     static constexpr int BAR_OFF = ANSWER_OFF + 16;
-    static constexpr int NBARS = 16 + 3 * SLOTS;
+    static constexpr int NBARS = 17 + 3 * SLOTS;
     static constexpr int TMEM_SLOT_OFF = BAR_OFF + NBARS * 8;
     static constexpr int ABORT_OFF = TMEM_SLOT_OFF + 4;
     static constexpr int USED = ABORT_OFF + 4;
@@ -87,14 +87,15 @@ struct PackedBwdPlan {
 };
 
 struct PackedBwdBars {
-    uint32_t a_full, a_empty, s_full, d_full, s_read, d_read, e0, e1, done, drain, drain2, answered, item_full, item_empty;
+    uint32_t a_full, a_empty, s_full, d_full, s_read, d_read, e1, done, drain, drain2, answered;
+    uint32_t e0, item_full, item_empty;      // [2] each (dK, dV: one e0)
     uint32_t full, empty, raw;       // [SLOTS]
 };
 
 template <int SLOTS>
 __device__ __forceinline__ PackedBwdBars packed_bars(uint32_t b) {
-    return {b,      b + 8,  b + 16, b + 24, b + 32, b + 40, b + 48,           b + 56,           b + 64,
-            b + 72, b + 80, b + 88, b + 96, b + 112, b + 128, b + 128 + 8 * SLOTS, b + 128 + 16 * SLOTS};
+    return {b,      b + 8,  b + 16,  b + 24,  b + 32,  b + 40,  b + 48,           b + 56,           b + 64,
+            b + 72, b + 80, b + 88, b + 104, b + 120, b + 136, b + 136 + 8 * SLOTS, b + 136 + 16 * SLOTS};
 }
 
 // done: issuing warps that end a gradient tile; readers: those that read a slot; takers:
@@ -102,7 +103,7 @@ __device__ __forceinline__ PackedBwdBars packed_bars(uint32_t b) {
 template <int SLOTS>
 __device__ __forceinline__ void packed_bars_init(const PackedBwdBars& m, int done, int readers, int takers) {
     for (uint32_t b : {m.a_full, m.a_empty, m.s_full, m.d_full, m.drain, m.drain2, m.answered}) mbar_init(b, 1);
-    for (uint32_t b : {m.s_read, m.d_read, m.e0, m.e1}) mbar_init(b, 4 * kGroups);
+    for (uint32_t b : {m.s_read, m.d_read, m.e0, m.e0 + 8, m.e1}) mbar_init(b, 4 * kGroups);
     mbar_init(m.done, done);
     for (int i = 0; i < kItems; ++i) {
         mbar_init(m.item_full + 8 * i, 1);
@@ -220,6 +221,9 @@ __device__ __forceinline__ void put_chunk(uint32_t t, int c, __nv_bfloat16* out,
 // of an item takes dP's place before its first dP.  Order of issue as dq_kernel's, but S_j
 // goes after dQ_{j-2}: whoever has S_j may then write its dS, where a wait for the dQ before
 // cost the elementwise warps 0.13 us a step (8192 tokens of 32 heads of 64: dQ 722 us, 738).
+// So a warp may be done with dS_{j+1} before another is with dS_j, and the two arrive on
+// barriers of their own: dS number u of a CTA on e0[u % 2].  Number u + 2 waits for dQ
+// number u, so it never arrives beside u.
 template <int NB, bool TAIL>
 __global__ void __launch_bounds__(kThreadsB, 1)
     packed_dq_kernel(const __grid_constant__ PackedBwdMaps maps, const __grid_constant__ PackedBwdArgs g) {
@@ -422,11 +426,11 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             t += uniform(it.all > 1);
             for (int j = 0; j < n; ++j, ++ne) {
                 const Slot s = first(t + j);
-                if (!warp_wait(m.full + 8 * s.s, s.ph, abort_flag) || !warp_wait(m.e0, ne & 1, abort_flag)) { ok = false; break; }
+                if (!warp_wait(m.full + 8 * s.s, s.ph, abort_flag) || !warp_wait(m.e0 + 8 * (ne & 1), (ne >> 1) & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 const uint32_t so = (s.s * P::TILE) >> 4;
                 if (one) {
-                    mma_accumulate<NB, TAIL, kCols / 2>(tmem + 384, tmem + 256 + 64 * ((t + j) & 1), k + so, ktl + so, j == 0);
+                    mma_accumulate<NB, TAIL, kCols / 2>(tmem + 384, tmem + 256 + 64 * (ne & 1), k + so, ktl + so, j == 0);
                     tc_commit(m.empty + 8 * s.s);
                     if (j + 1 == n) tc_commit(m.done);
                 }
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const uint64_t scale2 = f32x2(g.scale_log2, g.scale_log2);
         float* parts = reinterpret_cast<float*>(smem + P::SEL_OFF) + row;
         bool ok = true;
-        int t = 0;                    // steps so far
+        int ne = 0;                   // dS so far
         uint32_t par = 0;             // next parities: bit 0 s_full, 1 d_full, 2 e1, 3 done
         const auto row_lse = [&](const BwdItem& it) {
             const int i = it.tile * kTile + row;
@@ -513,9 +517,8 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                     if (c == lane) delta = __uint_as_float(r[c]);
                 neg_d = f32x2(-delta, -delta);
                 write_stats(delta);
-                ++t;
             }
-            for (int j = 0; j < n; ++j) {
+            for (int j = 0; j < n; ++j, ++ne) {
                 if (!warp_wait(m.s_full, par & 1, abort_flag)) { ok = false; break; }
                 tc_fence_after();
                 uint32_t r[32];
@@ -571,14 +574,13 @@ __global__ void __launch_bounds__(kThreadsB, 1)
                 for (int c = 0; c < 16; ++c) w[c] = pack_bf16x2(p[2 * c], p[2 * c + 1]);
                 // the last reader of dS's columns, the dQ two steps before, was done before S was
                 // issued (one of an item before: before that item's end)
-                tmem_st_32x32b_x16(tl + 256 + 64 * ((t + j) & 1) + kCols / 2 * e, w);
+                tmem_st_32x32b_x16(tl + 256 + 64 * (ne & 1) + kCols / 2 * e, w);
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(m.e0);
+                if (lane == 0) mbar_arrive(m.e0 + 8 * (ne & 1));
             }
             if (!ok) break;
-            t += n;
             // the next item's row statistic is on its way while this one's gradient is written
             // (its load would hold up that item's first step by a microsecond)
             const BwdItem& next = items[(item + 1) % kItems];
