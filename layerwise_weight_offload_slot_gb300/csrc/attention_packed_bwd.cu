@@ -175,10 +175,21 @@ __device__ __forceinline__ bool produce(const PackedBwdBars& m, BwdItem* items, 
     return put(end);
 }
 
-// The i-th item, by a warp that keeps it in registers and gives its place back.
+// warp_wait over `steps` steps of other warps, as warp 3 waits for an item's last tile: a
+// wait's limit for every 65536 of them (a step takes one or two us).  Those warps' own waits are
+// of one step each, so one that hangs ends this wait too.
+__device__ __forceinline__ bool long_wait(uint32_t bar, uint32_t parity, const volatile int* abort_flag, int steps) {
+    for (int k = steps >> 16;; --k) {
+        if (warp_wait(bar, parity, abort_flag)) return true;
+        if (k == 0 || __any_sync(0xFFFFFFFFu, *abort_flag)) return false;
+    }
+}
+
+// The i-th item, by a warp that keeps it in registers and gives its place back.  It comes
+// when all tiles of the one before are on their way: `steps` steps from now at most.
 __device__ __forceinline__ bool take_item(const PackedBwdBars& m, const BwdItem* items, int i, int lane, const volatile int* abort_flag,
-                                          BwdItem& it) {
-    if (!warp_wait(m.item_full + 8 * (i % kItems), (i / kItems) & 1, abort_flag)) return false;
+                                          BwdItem& it, int steps = 0) {
+    if (!long_wait(m.item_full + 8 * (i % kItems), (i / kItems) & 1, abort_flag, steps)) return false;
     it = items[i % kItems];
     __syncwarp();
     if (lane == 0) mbar_arrive(m.item_empty + 8 * (i % kItems));
@@ -446,14 +457,15 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         int t = 0;
         bool ok = true;
         BwdItem it;
+        it.n = 0;
         for (int i = 0;; ++i) {
-            ok = take_item(m, items, i, lane, abort_flag, it);
+            ok = take_item(m, items, i, lane, abort_flag, it, it.n);
             if (!ok || it.n < 0) break;
             if (it.n == 0) continue;
             t += (it.all > 1) + it.n;
             const int valid = it.nk - (it.i0 + it.n - 1) * kTile, s = first(t - 1).s;
             if (valid >= kTile) continue;
-            ok = warp_wait(m.raw + 8 * s, (par >> s) & 1u, abort_flag);
+            ok = long_wait(m.raw + 8 * s, (par >> s) & 1u, abort_flag, it.n);
             if (!ok) break;
             par ^= 1u << s;
             zero_rows<NB, TAIL>(smem + P::R_OFF + s * P::TILE, valid, lane, 32);
@@ -676,6 +688,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
     // This grid starts while packed_dq_kernel, whose every CTA has waited for what came
     // before, ends: all inputs are there, and only the row statistics need the wait (the
     // producer's, before the first of them) and what is written (the elementwise warps').
+    // The end of that grid is one of its items, however long: the warps that wait for
+    // the first statistics, or for room behind items without any, wait for it first, as
+    // their own waits are for a step.
     if (warp == 0) {
         // ---------------- producer: K and V, then Q with the row statistics, and dO
         PackedFlight in;
@@ -696,6 +711,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             const int steps = it.all * g.group, share = (steps + g.splits_k - 1) / g.splits_k;
             it.i0 = it.split * share;
             it.n = max(0, min(steps, it.i0 + share) - it.i0);
+            if (it.n == 0) pdl_wait();
             return true;
         };
         const auto load = [&](const BwdItem& it) -> bool {
@@ -753,6 +769,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const uint64_t rtl = sw32_desc(sb + P::R_OFF + NB * T::BLK);
         const uint64_t sel = sw32_desc(sb + P::SEL_OFF), stat = sw32_desc(sb + P::STAT_OFF);
         constexpr uint32_t id = idesc_bf16_f32(kTile, kTile);
+        pdl_wait();
         const auto full = [&](Slot s) { return warp_wait(m.full + 8 * s.s, s.ph, abort_flag); };
         // a slot is free when both products that read it are done: with one
         // issuer the later one's completion says so, with two each says its own
@@ -884,8 +901,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         int t = 0;
         bool ok = true;
         BwdItem it;
+        it.n = 0;
+        pdl_wait();
         for (int item = 0; ok; ++item) {
-            ok = take_item(m, items, item, lane, abort_flag, it);
+            ok = take_item(m, items, item, lane, abort_flag, it, it.n);
             if (!ok || it.n < 0) break;
             const int valid = it.nq - (it.first + it.all - 1) * kTile;
             if (it.n > 0 && valid < kTile) {
@@ -895,7 +914,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         const int s = u ? d.s : q.s;
-                        ok = ok && warp_wait(m.raw + 8 * s, (par >> s) & 1u, abort_flag);
+                        ok = ok && long_wait(m.raw + 8 * s, (par >> s) & 1u, abort_flag, it.all);
                         if (!ok) break;
                         par ^= 1u << s;
                         zero_rows<NB, TAIL>(smem + P::R_OFF + s * P::TILE, valid, lane, 32);
