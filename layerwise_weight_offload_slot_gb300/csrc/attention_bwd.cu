@@ -569,6 +569,9 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const uint64_t sel = sw32_desc(sb + P::SEL_OFF), stat = sw32_desc(sb + P::STAT_OFF);
         constexpr uint32_t id = idesc_bf16_f32(kTile, kTile);
         const auto full = [&](Slot t) { return warp_wait(m.full + 8 * t.s, t.ph, abort_flag); };
+        // the statistics that come with the first Q wait for dq_kernel's end, which may be
+        // far (its longest CTA); this warp's own waits are for a step
+        pdl_wait();
         // a slot is free when both products that read it are done: with one
         // issuer the later one's completion says so, with two each says its own
         const auto issue_s = [&](int i) -> bool {
@@ -682,6 +685,7 @@ __global__ void __launch_bounds__(kThreadsB, 1)
         const uint64_t scale2 = f32x2(g.scale_log2, g.scale_log2);
         bool ok = true;
         int qt = t0 + i0 % per;
+        pdl_wait();                   // as the issuers
         for (int i = 0; i < n; ++i) {
             const int lo = begin - (qt * kTile + kCols * e), hi = qlen - (qt * kTile + kCols * e);
             const bool cut = __any_sync(0xFFFFFFFFu, lo > 0 || hi < kCols);
