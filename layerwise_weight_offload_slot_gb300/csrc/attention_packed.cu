@@ -691,9 +691,10 @@ PackedGrid packed_grid(const dlo_attn_packed& a) {
     long long per = keys * (a.heads / p.gh) * (query_tiles > 0 ? query_tiles : 1) / (4 * kGb300Sms);
     if (per < kMinPer) per = kMinPer;
     if (per < (keys + parts - 1) / parts) per = (keys + parts - 1) / parts;
+    if (per >= keys) return p;                        // one part; from here on TK * per <= 2^30
     const long long ctas = static_cast<long long>(packed_slots(a.rows_k, a.batch, TK * static_cast<int>(per))) * (a.heads / p.gh);
     parts = (keys + per - 1) / per;
-    if (parts < 2 || ctas < 2 * p.ctas || ctas > 0x7FFFFFFF) return p;
+    if (ctas < 2 * p.ctas || ctas > 0x7FFFFFFF) return p;
     p.per = static_cast<int>(per);
     p.parts = static_cast<int>(parts);
     p.ctas = ctas;
