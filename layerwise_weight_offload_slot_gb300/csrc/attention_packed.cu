@@ -760,7 +760,7 @@ cudaError_t launch_attention_packed_fwd(const dlo_attn_packed& a, const void* Q,
     if (!map(&m.q, &m.qt, Q, a.rows_q, a.heads, a.ldq, plan.gh) || !map(&m.k, &m.kt, K, a.rows_k, a.kv_heads, a.ldk, 1) ||
         !map(&m.v, &m.vt, V, a.rows_k, a.kv_heads, a.ldv, 1))
         return cudaErrorInvalidValue;
-    const bool duo = plan.ctas > kGb300Sms;           // fewer: nothing would share an SM
+    const bool duo = attn_duo_enabled() && plan.ctas > kGb300Sms;       // fewer: nothing would share an SM
     cudaError_t e;
     if (hd <= 64) e = duo ? run_packed<1, false, true>(m, g, s, launches) : run_packed<1, false, false>(m, g, s, launches);
     else if (tail) e = duo ? run_packed<1, true, true>(m, g, s, launches) : run_packed<1, true, false>(m, g, s, launches);

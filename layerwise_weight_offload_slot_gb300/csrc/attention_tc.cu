@@ -562,17 +562,15 @@ cudaError_t run_tc(const void* Q, const void* K, const void* V, void* O, int bat
     return le_ != cudaSuccess ? le_ : cudaGetLastError();
 }
 
-// DLO_ATTN_DUO=0 keeps head dims up to 80 on one CTA per SM (tuning).
-bool attn_duo_enabled() {
-    static int v = -1;
-    if (v < 0) {
-        const char* e = std::getenv("DLO_ATTN_DUO");
-        v = (e && e[0] == '0') ? 0 : 1;
-    }
-    return v != 0;
-}
-
 }  // namespace
+
+bool attn_duo_enabled() {
+    static const bool on = [] {
+        const char* e = std::getenv("DLO_ATTN_DUO");
+        return !(e && e[0] == '0');
+    }();
+    return on;
+}
 
 bool attention_tc_supported(int hd) { return hd >= 8 && hd <= 128 && hd % 8 == 0; }
 

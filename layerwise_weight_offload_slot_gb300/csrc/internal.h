@@ -255,7 +255,10 @@ cudaError_t launch_attention_bwd(const dlo_attn& a, const void* Q, const void* K
                                  const float* lse, const void* dO, void* dQ, void* dK, void* dV, void* ws, int* err,
                                  cudaStream_t s, unsigned long long* launches);
 
-// Operators for packed batches (attention_tc.cu, attention_bwd.cu, packed.cu).
+// DLO_ATTN_DUO=0 keeps attention with head dims up to 80 on one CTA per SM (tuning).
+bool attn_duo_enabled();
+
+// Operators for packed batches (attention_packed.cu, attention_packed_bwd.cu, packed.cu).
 size_t attention_packed_fwd_workspace(const dlo_attn_packed& a);
 size_t attention_packed_bwd_workspace(const dlo_attn_packed& a);
 cudaError_t launch_attention_packed_fwd(const dlo_attn_packed& a, const void* Q, const void* K, const void* V, void* O,
