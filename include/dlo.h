@@ -699,15 +699,17 @@ typedef struct dlo_rope {
 } dlo_rope;
 
 /* The table of the two ops below: step of pair p = f_p / 2 pi as a 64-bit fraction
- * of a turn.  Host memory; n must be the number of pairs (the dims' sum / 2).  A
- * program lays it out once and keeps it on the device. */
+ * of a turn, formed in 64-bit floats.  Host memory; n must be the number of pairs (the
+ * dims' sum / 2).  A program lays it out once and keeps it on the device. */
 dlo_status dlo_rope_steps(const dlo_rope* r, uint64_t* steps, int n);
 
 /* y = x (bf16 [rows], `heads` heads from the pointer's column on) turned by its
  * rows' positions (int32 [rows, axes], any value); q and k that lie side by side
- * in fused rows are one call.  In place: y = x and ldy = ldx.  Angles are exact
- * to 2^-32 of a turn.  ld % 8 == 0 and at least the row; x, y 16-byte, steps
- * (device) 8-byte, positions 4-byte aligned. */
+ * in fused rows are one call.  In place: y = x and ldy = ldx.  An angle is off by
+ * 2^-26 of a turn at most, as a float holds it, and by what the table is: 2^-52
+ * |position| of a turn (2^-51 for the two blended scalings, with fast >= 2 slow and
+ * length >= 2 pi fast), 2^-21 at the ends of int32.  ld % 8 == 0 and at least the
+ * row; x, y 16-byte, steps (device) 8-byte, positions 4-byte aligned. */
 dlo_status dlo_op_rope_fwd(const dlo_rope* r, const void* x, const int* positions, const uint64_t* steps, int rows,
                            void* y, void* stream);
 

@@ -88,9 +88,11 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const int* grids, co
 // Pair p of a row at position n turns by n f_p: (u, v) -> amp (u c - v s, u s + v c).
 //
 // The angle is kept in turns as a 64-bit fraction: step = f_p / 2 pi * 2^64, and
-// n step mod 2^64 is the exact fraction of a turn for any 32-bit n, negative ones
-// too, where a 32-bit float product is off by 2^-24 of the whole angle (0.06 rad at
-// position 10^6).  Its upper 32 bits go to sincospi: off by 2^-25 of a half turn.
+// n step mod 2^64 loses nothing for any 32-bit n, negative ones too, where a 32-bit
+// float product is off by 2^-24 of the whole angle (0.06 rad at position 10^6).  What is
+// left is the table's error, n times (up to 2^-24 of a turn at n = 2^31, measured; its bound
+// is at dlo_rope_steps), and that the upper 32 bits go to sincospi as a float: off by
+// 2^-25 of a half turn.
 //
 // Bound by memory: x is read and y written once, 16 bytes a thread where the pairs
 // allow it.  A row's sines and cosines are formed once, in shared memory, while the

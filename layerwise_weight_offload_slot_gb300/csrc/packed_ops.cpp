@@ -91,6 +91,9 @@ extern "C" dlo_status dlo_op_packed_plan(const int* grids, const int* offsets, i
                                         static_cast<cudaStream_t>(stream), Uncounted()));
 }
 
+// A step's error in turns, u = 2^-53: the exponent, pow (2 u), the divisions and 2 pi leave
+// f u (|ln f| + 4), a factor or base up to 3 u f more, over 2 pi: less than 2 u, as f <= 1.  Blended,
+// k of f length / 2 pi <= fast turns adds 2 u (|ln f| + 7) f with fast >= 2 slow: less than 4 u in all.
 extern "C" dlo_status dlo_rope_steps(const dlo_rope* r, uint64_t* steps, int n) {
     if (const char* m = rope_problem(r)) return inval(m);
     if (!steps) return inval("NULL steps");
