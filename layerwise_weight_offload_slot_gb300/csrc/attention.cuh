@@ -179,7 +179,8 @@ __device__ __forceinline__ void packed_other(const int* starts, int b, int rows,
 }
 
 // One past the last key that query i sees (off = nk - nq, cb = causal block,
-// 0: none): floor((i + off) / cb) >= floor(j / cb).  cb <= nk.
+// 0: none): floor((i + off) / cb) >= floor(j / cb).  cb is at most the rows of K, so 2^30:
+// nothing here passes 2^31.
 __device__ __forceinline__ int key_end(int i, int off, int cb, int klen) {
     if (cb == 0) return klen;
     const int t = i + off;

@@ -16,13 +16,6 @@ constexpr int kThreadsB = 128 + 32 * 4 * kGroups;
 // three bf16 parts of -L, 3..5 those of -D.
 constexpr int kStatBytes = kTile * 32;
 
-struct BwdMaps {
-    CUtensorMap q, k, v, d;       // 64-column boxes, 128-byte swizzle (d: dO)
-    CUtensorMap qt, kt, vt, dt;   // 16-column tails, 32-byte swizzle
-    CUtensorMap gq, gk, gv;       // the gradients, likewise
-    CUtensorMap gqt, gkt, gvt;
-};
-
 // Shared memory of one CTA: two tiles that stay (Q and dO; K and V), slots for the
 // two streams of tiles that move (K and V; Q and dO), and per-row values.
 //
@@ -96,52 +89,6 @@ struct DkvTmem {
     static_assert(DK_COL + HDP <= 512, "attention backward tensor memory plan");
 };
 
-struct BwdBars {
-    uint32_t a_full, raw0, raw1, s_full, drain2, d_full, e0, e1, done, drain, s_read, d_read, staged, full, empty;
-};
-
-template <int SLOTS>
-__device__ __forceinline__ BwdBars bwd_bars(uint32_t b) {
-    return {b, b + 8, b + 16, b + 24, b + 32, b + 40, b + 48, b + 56, b + 64, b + 72, b + 80, b + 88,
-            b + 96, b + 104, b + 104 + 8 * SLOTS};
-}
-
-template <int SLOTS>
-__device__ __forceinline__ void bwd_init(const BwdBars& m, int done, int readers) {
-    mbar_init(m.a_full, 1);
-    mbar_init(m.raw0, 1);
-    mbar_init(m.raw1, 1);
-    mbar_init(m.s_full, 1);
-    mbar_init(m.d_full, 1);
-    mbar_init(m.e0, 4 * kGroups);
-    mbar_init(m.e1, 4 * kGroups);
-    mbar_init(m.s_read, 4 * kGroups);
-    mbar_init(m.d_read, 4 * kGroups);
-    mbar_init(m.staged, 4 * kGroups);
-    mbar_init(m.done, done);
-    mbar_init(m.drain, 1);
-    mbar_init(m.drain2, 1);
-    for (int i = 0; i < SLOTS; ++i) {
-        mbar_init(m.full + 8 * i, 1);
-        mbar_init(m.empty + 8 * i, readers);
-    }
-    fence_mbar_init();
-}
-
-// Loads in flight, for the drain: slots and the parity of each.
-struct InFlight {
-    uint32_t on = 0, par = 0;
-    __device__ void add(Slot s) {
-        on |= 1u << s.s;
-        par = (par & ~(1u << s.s)) | (s.ph << s.s);
-    }
-    template <int SLOTS>
-    __device__ void drain(uint32_t full) const {
-        for (int i = 0; i < SLOTS; ++i)
-            if (on & (1u << i)) mbar_wait(full + 8 * i, (par >> i) & 1u, nullptr);
-    }
-};
-
 // 128 x 128 (+)= A B^T over the head dim, both operands K-major in shared memory.
 template <int NB, bool TAIL>
 __device__ __forceinline__ void mma_scores(uint32_t d, uint64_t a, uint64_t at, uint64_t b, uint64_t bt) {
@@ -176,50 +123,6 @@ __device__ __forceinline__ void split3(float x, uint32_t& hi_mid, uint32_t& lo) 
     const float b = __bfloat162float(__float2bfloat16_rn(x - a));
     hi_mid = pack_bf16x2(a, b);
     lo = __bfloat16_as_ushort(__float2bfloat16_rn(x - a - b));
-}
-
-// One thread's part of an accumulator row (32-column chunks first, first +
-// step, ...) times `scale`: in fp32 to `part` if that is set, else in bf16 to the
-// tile in shared memory that TMA then stores (rows and columns past the tensor
-// are not written).  `none`: zeros instead, for a row without a visible pair; its
-// accumulator is 0, or NaN where the tile's other rows met an infinity.
-template <int NB, bool TAIL>
-__device__ __forceinline__ void store_row(uint32_t t, uint8_t* tile, int row, float* part, int hd, bool live, bool none, float scale,
-                                          int first, int step) {
-#pragma unroll 1
-    for (int c = first; c < (AttnTile<NB, TAIL>::HDP + 31) / 32; c += step) {
-        uint32_t r[32], w[16];
-        tmem_ld_32x32b_x32(t + c * 32, r);
-        tmem_wait_ld_r(r);
-        if (none) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) r[k] = 0;
-        }
-        if (part) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (live && c * 32 + 4 * k < hd)
-                    *reinterpret_cast<float4*>(part + c * 32 + 4 * k) =
-                        make_float4(__uint_as_float(r[4 * k]) * scale, __uint_as_float(r[4 * k + 1]) * scale,
-                                    __uint_as_float(r[4 * k + 2]) * scale, __uint_as_float(r[4 * k + 3]) * scale);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
-            put_row<NB, TAIL>(tile, row, c, w);
-        }
-    }
-}
-
-__device__ __forceinline__ float dot8(uint4 a, uint4 b) {
-    const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
-    float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 u = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x[i]));
-        const float2 v = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&y[i]));
-        t += u.x * v.x + u.y * v.y;
-    }
-    return t;
 }
 
 // The end of an issuing warp: on an abort, its MMAs in flight are waited for.
