@@ -19,7 +19,7 @@
 // What bounds it: for long sequences the tensor core and, in dQ, the elementwise warps'
 // chain of waits, loads and stores (1.13 us a step at head dim 128; attention_bwd.cu's
 // kernels, whose loops know where their slots begin, are 5% faster there: 8192 tokens, 40
-// heads, 2600 us, these 2720); for short ones the change of items, ~3 us each: the last
+// heads, 2600 us, these 2735); for short ones the change of items, ~3 us each: the last
 // product, the gradient's way out (~0.9), K and V (Q, dO and O) from L2 (1.2) and the first
 // products.  16 x 512 tokens of 40 heads of 128: 261 us (dQ 132, tensor pipe 46% active; dK, dV
 // 140, 55%), 393 with a CTA an item.
