@@ -402,7 +402,10 @@ __global__ void __launch_bounds__(kThreadsB, 1)
             ++na;
             if (ok && lead) {
                 const Slot o = first(t), v = second(t);
-                ok = (nd == 0 || warp_wait(m.d_read, (nd - 1) & 1, abort_flag)) && warp_wait(m.full + 8 * o.s, o.ph, abort_flag);
+                // V's slot too, into which nothing comes: given back before the producer has had
+                // it, its `empty` could pass two phases between two looks of the producer
+                ok = (nd == 0 || warp_wait(m.d_read, (nd - 1) & 1, abort_flag)) && warp_wait(m.full + 8 * o.s, o.ph, abort_flag) &&
+                     warp_wait(m.full + 8 * v.s, v.ph, abort_flag);
                 if (ok) {
                     ++nd;
                     tc_fence_after();

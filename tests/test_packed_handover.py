@@ -111,3 +111,86 @@ def test_every_order_hands_each_step_over_whole(items):
 
 def test_the_model_finds_the_mistake_of_one_barrier():
     assert "dQ reads another step's dS" in mistakes((3,), 1)
+
+
+# ------------------------------------------------------------------ slots
+#
+# The producer, the two issuing warps and the elementwise ones (as one) over the slots of the ring.  An item of more
+# than one key tile begins with a step for D, which takes O in the first stream's slot and nothing in the second's.
+
+def lead_waits_for_both_slots():
+    """Whether D's product waits for the producer to have had the second slot too, from the source."""
+    with open(os.path.join(CSRC, "attention_packed_bwd.cu")) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    lead = re.search(r"if \(ok && lead\) \{\s*const Slot o = first\(t\), v = second\(t\);\s*ok = \(nd == 0.*?if \(ok\) \{", text, re.S).group()
+    assert "m.full + 8 * o.s" in lead
+    return "m.full + 8 * v.s" in lead
+
+
+def slot(shared, second, i):
+    """Slot and how often it was used before, of tile i of a stream (attention_bwd.cuh: slot_of)."""
+    if not shared:
+        return i % 3 + (3 if second else 0), i // 3
+    if second:                          # slots 2.. begin with this stream: their first tile is number 0
+        return (i + 2) % 5, 2 * (i // 5) + (1 if i % 5 >= 3 else 0)
+    return i % 5, 2 * (i // 5) + (1 if i % 5 >= 2 else 0)
+
+
+def ring_roles(items, shared, both):
+    """As roles(), for items given by their key tiles, or (1, True) for a single one of several."""
+    load, issue, grad, work = [], [], [], []
+    uses = {}
+    t = s = d = 0                       # steps, S and dP so far
+    for i, n in enumerate(items):
+        n, lead = n if isinstance(n, tuple) else (n, n > 1)
+        for j in range(n + lead):
+            (k, ku), (v, vu) = slot(shared, False, t + j), slot(shared, True, t + j)
+            for x, u in ((k, ku), (v, vu)):
+                uses.setdefault(x, []).append(u)
+                if u:
+                    load.append(("wait", ("empty", x), u - 1))
+                load.append(("arrive", ("full", x)))
+        if lead:
+            (o, ou), (v, vu) = slot(shared, False, t), slot(shared, True, t)
+            issue += [("wait", "d_read", d - 1)] if d else []
+            issue += [("wait", ("full", o), ou)] + ([("wait", ("full", v), vu)] if both else [])
+            issue += [("arrive", "d_full"), ("arrive", ("empty", o)), ("arrive", ("empty", v))]
+            work += [("wait", "d_full", d), ("arrive", "d_read")]
+            d += 1
+        t += lead
+        for j in range(n):
+            (k, ku), (v, vu) = slot(shared, False, t + j), slot(shared, True, t + j)
+            issue += [("wait", "s_read", s - 1)] if s else []
+            issue.append(("wait", ("full", k), ku))
+            if j >= 2:
+                b, bu = slot(shared, False, t + j - 2)
+                issue.append(("wait", ("empty", b), bu))
+            issue += [("arrive", "s_full")] + ([("wait", "d_read", d - 1)] if d else [])
+            issue += [("wait", ("full", v), vu), ("arrive", "d_full"), ("arrive", ("empty", v))]
+            work += [("wait", "s_full", s), ("arrive", "s_read"), ("wait", "d_full", d), ("arrive", "d_read"), ("arrive", ("e0", s % 2))]
+            grad += [("wait", ("full", k), ku), ("wait", ("e0", s % 2), s // 2), ("arrive", ("empty", k))]
+            s, d = s + 1, d + 1
+        grad.append(("arrive", "done"))
+        work.append(("wait", "done", i))
+        t += n
+    assert all(u == list(range(len(u))) for u in uses.values())       # every use of a slot follows the one before
+    return [load, issue, grad, work]
+
+
+def ring_mistakes(items, shared, both, monkeypatch):
+    monkeypatch.setitem(globals(), "roles", lambda *_: ring_roles(items, shared, both))
+    monkeypatch.setitem(globals(), "arrivals", lambda _: 1)
+    return mistakes(items, 2)
+
+
+RINGS = [(5,), (2, 2, 3), (1, 1, 1, 1, 2, 1), (1, 4, 1, 2), (3, 1, 1, 1, 3), (1, 2, 1, 1, 1, 6), ((1, True), 1, (1, True), (1, True), 2)]
+
+
+@pytest.mark.parametrize("shared", [False, True], ids=["two rings", "one ring"])
+@pytest.mark.parametrize("items", RINGS, ids=str)
+def test_every_order_hands_each_slot_over(items, shared, monkeypatch):
+    assert ring_mistakes(items, shared, lead_waits_for_both_slots(), monkeypatch) == set()
+
+
+def test_the_model_finds_the_slot_that_is_given_back_unseen(monkeypatch):
+    assert any(ring_mistakes(items, shared, False, monkeypatch) for items in RINGS for shared in (False, True))
